@@ -24,7 +24,7 @@
  *     default stream) and never synchronises.
  *   - Every call returns an hq_status and never aborts.  Argument errors are
  *     detected on the host before any launch.  Errors that can only be seen
- *     on the device (an expert id out of range, a pipeline wait that timed
+ *     on the device (an index out of range, a pipeline wait that timed
  *     out) are recorded in a per-device error word read by hq_device_error().
  *   - Row-major layouts; `[a, b]` means a rows of b contiguous elements.
  *   - Tensors the library consumes are in the "standard format":
@@ -75,7 +75,7 @@ typedef enum {
   HQ_ERR_WORKSPACE = 3,    /* workspace smaller than *_workspace_bytes()   */
   HQ_ERR_CUDA = 4,         /* a CUDA runtime call or launch failed         */
   HQ_ERR_TIMEOUT = 5,      /* a bounded device-side wait gave up           */
-  HQ_ERR_DEVICE_INDEX = 6, /* an expert id outside [0, E) seen on device   */
+  HQ_ERR_DEVICE_INDEX = 6, /* expert id, slot, page, length or position out of range on device */
   HQ_ERR_ARCH = 7          /* the current device is not sm_100             */
 } hq_status;
 
@@ -441,6 +441,137 @@ HQ_API hq_status hq_moe_unpermute_sum(int T, int topk, int N, const void *y_bf16
 HQ_API hq_status hq_gemm_noalloc(const hq_quant_desc *desc, int M, int N, int K, const void *packed_w,
                                  const void *a, const void *a_scales, const float *a_global, void *c_bf16,
                                  hq_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Decoder cache (an addition of this library): what a serving step needs
+ * between the QKV product and the output product.  Rotary positions are put
+ * into q and k, the new keys and values are quantised into a paged cache
+ * with hq_quant_act's recipes, and one new token per sequence attends over
+ * it.  All tensors are bf16 with unit stride along the channels; strides
+ * between tokens (and heads, where given) are in elements, non-negative and
+ * multiples of 8, so that q, k and v may be parts of one projection's output.
+ * Pointers and the stream belong to the current device.
+ * ---------------------------------------------------------------------- */
+
+/* How the frequencies of a rotation are scaled for contexts longer than the
+ * one trained for.  f_i = base^(-2i / rot_dim), i < rot_dim / 2, radians per
+ * position, is the plain frequency; y is the share of it that is kept and
+ * f'_i = f_i (y + (1 - y) / factor):
+ *   PLAIN   f' = f
+ *   LINEAR  f' = f / factor
+ *   TURNS   y = clamp((context f / 2pi - low) / (high - low), 0, 1): by the
+ *           turns over the original context, fewer than `low` fully scaled
+ *   INDEX   y = 1 - clamp((i - a) / max(c - a, 0.001), 0, 1) with
+ *           a = max(floor(at(high)), 0), c = min(ceil(at(low)), rot_dim - 1),
+ *           at(n) = rot_dim ln(context / (2pi n)) / (2 ln base): a ramp over
+ *           the index between the frequencies of `high` and `low` turns */
+typedef enum { HQ_ROPE_PLAIN = 0, HQ_ROPE_LINEAR = 1, HQ_ROPE_TURNS = 2, HQ_ROPE_INDEX = 3 } hq_rope_scaling;
+
+/* A rotation.  Zero-initialise; base, factor, low, high, scaling, context and
+ * amplitude are used by hq_rope_table alone. */
+typedef struct {
+  int32_t rot_dim;     /* channels rotated: the first rot_dim of a head, even, 2..head width   */
+  int32_t interleaved; /* 0: channel i pairs with i + rot_dim / 2; 1: channel 2i with 2i + 1   */
+  int32_t scaling;     /* hq_rope_scaling                                                      */
+  int32_t context;     /* original context in tokens (TURNS, INDEX), >= 1                      */
+  double base;         /* > 1                                                                  */
+  double factor;       /* > 0 (LINEAR, TURNS, INDEX)                                           */
+  double low, high;    /* turns, 0 < low < high (TURNS, INDEX)                                 */
+  double amplitude;    /* multiplies cosine and sine; 0 = 1                                    */
+} hq_rope_desc;
+
+/* table fp32 [P, rot_dim]: row p holds amplitude * cos(p f'_i) for
+ * i < rot_dim / 2, then amplitude * sin(p f'_i); angles in 64 bits, reduced
+ * before they are rounded.  Built once; P >= 0. */
+HQ_API hq_status hq_rope_table(const hq_rope_desc *rope, int P, float *table, hq_stream_t stream);
+
+/* Rotates x [T, H, D] into out [T, H, D]: with c, s from row positions[t]
+ * (device int32 [T], values in [0, P)) of `table`, each pair (a, b) becomes
+ * (a c - b s, b c + a s), every step an fp32 operation, rounded to bf16 at the
+ * end; channels from rot_dim on are copied.  out may be x with the same
+ * strides; other overlaps are not allowed.  D a multiple of 8, at most 1024.
+ * A position outside [0, P) sets HQ_ERR_DEVICE_INDEX in the device error word
+ * and leaves the token's out row as it was.  (The inverse rotation, which is
+ * also the gradient, takes a table with the sines negated.) */
+HQ_API hq_status hq_rope(const hq_rope_desc *rope, int T, int H, int D, const void *x_bf16, int64_t x_token_stride,
+                         int64_t x_head_stride, const int32_t *positions, const float *table, int P,
+                         void *out_bf16, int64_t out_token_stride, int64_t out_head_stride, hq_stream_t stream);
+
+/* A paged key-value cache of one layer.  The caller owns `pages`, a buffer of
+ * num_pages * hq_kv_page_bytes() bytes (16-byte aligned; its contents need no
+ * initialisation), and hands out page ids 0..num_pages - 1.  Slot
+ * page * page_size + i is token i of a page; keys and values of all heads of
+ * a token are in its slot.  The layout inside a page is opaque and depends on
+ * the whole description.  What is held, per token and head:
+ *   HQ_BF16   the bf16 values
+ *   HQ_E4M3   E4M3 codes and one fp32 scale: hq_quant_act's per-token recipe
+ *             on the head's channels (s = amax / 448, 1 for an all-zero row)
+ *   HQ_NVFP4  E2M1 codes and a UE4M3 scale per 16 channels under a static
+ *             second-level scale: hq_quant_act's recipe with static_global;
+ *             global_scale is device fp32 [2], for K and for V, each > 0,
+ *             and the same in every call on a cache (NULL for the others)
+ * Zero-initialise the struct. */
+typedef struct {
+  int32_t dtype;     /* HQ_BF16 | HQ_E4M3 | HQ_NVFP4 */
+  int32_t heads;     /* kv heads, 1..1024             */
+  int32_t head_dim;  /* 64 | 128 | 192 | 256          */
+  int32_t page_size; /* tokens per page: a multiple of 16, at most 4096 */
+  int32_t reserved[4];
+} hq_kv_desc;
+
+/* Bytes of one page (0 if the description is not supported). */
+HQ_API size_t hq_kv_page_bytes(const hq_kv_desc *kv);
+
+/* Writes T tokens: k, v [T, heads, head_dim] (heads adjacent) into
+ * slots[t] (device int64 [T]).  A negative slot skips its token (padding); a
+ * slot past the last page sets HQ_ERR_DEVICE_INDEX and skips it.  Two tokens
+ * of a call in one slot leave that slot's contents unspecified.  Nothing but
+ * the named slots changes. */
+HQ_API hq_status hq_kv_write(const hq_kv_desc *kv, int T, const void *k_bf16, int64_t k_stride, const void *v_bf16,
+                             int64_t v_stride, const int64_t *slots, const float *global_scale, int num_pages,
+                             void *pages, hq_stream_t stream);
+
+/* hq_kv_write with positions, in one launch: k is rotated (hq_rope's steps;
+ * the fp32 result is what is quantised or rounded) and, with q_heads > 0,
+ * q [T, q_heads, head_dim] is rotated into q_out as hq_rope does (q_out may be
+ * q).  A token with a slot that is skipped still has its q rotated; a position
+ * outside [0, P) sets HQ_ERR_DEVICE_INDEX, and the token is neither written
+ * nor its q rotated.  q_heads == 0: q and q_out are NULL. */
+HQ_API hq_status hq_rope_kv_write(const hq_rope_desc *rope, const hq_kv_desc *kv, int T, int q_heads,
+                                  const void *q_bf16, int64_t q_stride, void *q_out_bf16, int64_t q_out_stride,
+                                  const void *k_bf16, int64_t k_stride, const void *v_bf16, int64_t v_stride,
+                                  const int32_t *positions, const float *table, int P, const int64_t *slots,
+                                  const float *global_scale, int num_pages, void *pages, hq_stream_t stream);
+
+/* Reads T slots back: k_out, v_out [T, heads, head_dim], the held values
+ * rounded to bf16; either may be NULL.  A negative slot leaves its row as it
+ * was, one past the last page also sets HQ_ERR_DEVICE_INDEX. */
+HQ_API hq_status hq_kv_read(const hq_kv_desc *kv, int T, const int64_t *slots, const float *global_scale,
+                            int num_pages, const void *pages, void *k_out_bf16, int64_t k_stride, void *v_out_bf16,
+                            int64_t v_stride, hq_stream_t stream);
+
+/* Attention of one new token per sequence over the cache.  Sequence b has
+ * lengths[b] tokens (device int32 [B], the new one among them, already
+ * written); its token j is token j % page_size of page
+ * page_table[b, j / page_size] (device int32 [B, max_pages]; entries past the
+ * length are not read).  Query head i uses kv head i / (q_heads / heads);
+ * q_heads is a multiple of heads.  With x_j = scale * q . k_j over
+ * max(0, length - window) <= j < length (window 0: all of them),
+ *   out[b, i] = sum_j exp(x_j) v_j / sum_j exp(x_j)   bf16 [B, q_heads, head_dim]
+ *   lse[b, i] = ln sum_j exp(x_j)                     fp32 [B, q_heads], may be NULL
+ * A length of 0 gives out = 0 and lse = -inf.  A length below 0 or above
+ * max_pages * page_size sets HQ_ERR_DEVICE_INDEX and counts as 0 or as that
+ * bound; a page id outside the cache sets it too and its tokens are left out.
+ * Slots past a length may hold anything.  Scores, softmax and sums are fp32;
+ * the result does not depend on timing.  `workspace` as for hq_gemm: of
+ * hq_paged_attn_workspace_bytes() bytes, its counters zero when first used and
+ * left zero by every completed call; calls that share one must be ordered. */
+HQ_API size_t hq_paged_attn_workspace_bytes(const hq_kv_desc *kv, int B, int q_heads);
+HQ_API hq_status hq_paged_attn(const hq_kv_desc *kv, int B, int q_heads, const void *q_bf16, int64_t q_stride,
+                               const float *global_scale, int num_pages, const void *pages,
+                               const int32_t *page_table, int max_pages, const int32_t *lengths, float scale,
+                               int window, void *out_bf16, int64_t out_stride, float *lse, void *workspace,
+                               size_t ws_bytes, hq_stream_t stream);
 
 #ifdef __cplusplus
 }

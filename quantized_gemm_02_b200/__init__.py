@@ -16,17 +16,21 @@ __all__ = [
     "HQ_BF16", "HQ_FP32", "HQ_INT4", "HQ_UINT4", "HQ_E2M1", "HQ_E4M3", "HQ_E8M0", "HQ_UE4M3", "HQ_MXFP8",
     "HQ_NVFP4", "HQ_INT2", "HQ_UINT2", "HQ_INT3", "HQ_UINT3", "HQ_E2M3", "HQ_E3M2", "HQ_E0M3", "HQ_INT1", "HQ_UINT1",
     "HQ_MOE_GROUPED", "HQ_MOE_INDEXED",
+    "RopeDesc", "KVDesc", "HQ_ROPE_PLAIN", "HQ_ROPE_LINEAR", "HQ_ROPE_TURNS", "HQ_ROPE_INDEX",
     "hq_status_string", "hq_device_error", "hq_packed_weights_bytes", "hq_pack_weights", "hq_unpack_weights",
     "hq_quant_act", "hq_gemm_workspace_bytes", "hq_gemm", "hq_gemm_config_workspace_bytes",
     "hq_gemm_config", "hq_gemm_plan", "hq_moe_plan", "hq_moe_permute", "hq_moe_workspace_bytes",
     "hq_moe_gemm", "hq_moe_masked_workspace_bytes", "hq_moe_gemm_masked", "hq_silu_and_mul", "hq_moe_unpermute_sum",
     "hq_gemm_noalloc", "hq_selftest_wait_timeout", "hq_pack_weights_gated", "hq_unpack_weights_gated",
     "hq_moe_gated_workspace_bytes", "hq_moe_gemm_gated",
+    "hq_rope_table", "hq_rope", "hq_kv_page_bytes", "hq_kv_write", "hq_rope_kv_write", "hq_kv_read",
+    "hq_paged_attn_workspace_bytes", "hq_paged_attn",
 ]
 
 HQ_BF16, HQ_FP32, HQ_INT4, HQ_UINT4, HQ_E2M1, HQ_E4M3, HQ_E8M0, HQ_UE4M3, HQ_MXFP8, HQ_NVFP4 = range(10)
 HQ_INT2, HQ_UINT2, HQ_INT3, HQ_UINT3, HQ_E2M3, HQ_E3M2, HQ_E0M3, HQ_INT1, HQ_UINT1 = range(10, 19)
 HQ_MOE_GROUPED, HQ_MOE_INDEXED = 0, 1
+HQ_ROPE_PLAIN, HQ_ROPE_LINEAR, HQ_ROPE_TURNS, HQ_ROPE_INDEX = range(4)
 
 STATUS = {
     0: "HQ_OK", 1: "HQ_ERR_INVALID_ARG", 2: "HQ_ERR_UNSUPPORTED", 3: "HQ_ERR_WORKSPACE", 4: "HQ_ERR_CUDA",
@@ -41,6 +45,8 @@ EXPORTS = (
     "hq_moe_gemm", "hq_moe_masked_workspace_bytes", "hq_moe_gemm_masked", "hq_silu_and_mul", "hq_moe_unpermute_sum",
     "hq_gemm_noalloc", "hq_selftest_wait_timeout", "hq_pack_weights_gated", "hq_unpack_weights_gated",
     "hq_moe_gated_workspace_bytes", "hq_moe_gemm_gated",
+    "hq_rope_table", "hq_rope", "hq_kv_page_bytes", "hq_kv_write", "hq_rope_kv_write", "hq_kv_read",
+    "hq_paged_attn_workspace_bytes", "hq_paged_attn",
 )
 
 
@@ -80,6 +86,19 @@ class PlanInfo(ctypes.Structure):
                                                 "ctas")}
 
 
+class RopeDesc(ctypes.Structure):
+    """hq_rope_desc: a rotation and how its frequencies are scaled."""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("context", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
+class KVDesc(ctypes.Structure):
+    """hq_kv_desc: a paged key-value cache."""
+    _fields_ = [("dtype", ctypes.c_int32), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("reserved", ctypes.c_int32 * 4)]
+
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 
 
@@ -100,6 +119,7 @@ def _lib() -> ctypes.CDLL:
         P, I, Z, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
         D = ctypes.POINTER(QuantDesc)
         C = ctypes.POINTER(ComputeConfig)
+        R, V, LL = ctypes.POINTER(RopeDesc), ctypes.POINTER(KVDesc), ctypes.c_longlong
         sig = {
             "hq_status_string": (ctypes.c_char_p, [I]),
             "hq_device_error": (I, [P]),
@@ -126,6 +146,14 @@ def _lib() -> ctypes.CDLL:
             "hq_unpack_weights_gated": (I, [D, I, I, I, P, P, P, P, P, P]),
             "hq_moe_gated_workspace_bytes": (Z, [I, D, I, I, I, I, I]),
             "hq_moe_gemm_gated": (I, [I, D, I, I, I, I, I, P, P, P, P, P, P, P, P, P, Z, P]),
+            "hq_rope_table": (I, [R, I, P, P]),
+            "hq_rope": (I, [R, I, I, I, P, LL, LL, P, P, I, P, LL, LL, P]),
+            "hq_kv_page_bytes": (Z, [V]),
+            "hq_kv_write": (I, [V, I, P, LL, P, LL, P, P, I, P, P]),
+            "hq_rope_kv_write": (I, [R, V, I, I, P, LL, P, LL, P, LL, P, LL, P, P, I, P, P, I, P, P]),
+            "hq_kv_read": (I, [V, I, P, P, I, P, P, LL, P, LL, P]),
+            "hq_paged_attn_workspace_bytes": (Z, [V, I, I]),
+            "hq_paged_attn": (I, [V, I, I, P, LL, P, I, P, P, I, P, F, I, P, LL, P, P, Z, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -304,3 +332,77 @@ def hq_moe_gemm_gated(mode, desc, T, topk, E, I, K, packed_w, a, a_scales, a_glo
     _check("hq_moe_gemm_gated", _lib().hq_moe_gemm_gated(
         mode, ctypes.byref(desc), T, topk, E, I, K, _ptr(packed_w), _ptr(a), _ptr(a_scales), _ptr(a_global),
         _ptr(topk_ids), _ptr(expert_offsets), _ptr(perm), _ptr(out), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def _on_device(fn, *tensors):
+    """Device pointers of tensors (None and integer addresses pass): each has
+    to be on the current CUDA device, whose stream the call runs on."""
+    import torch
+    dev = torch.cuda.current_device() if any(hasattr(t, "data_ptr") and t.is_cuda for t in tensors) else -2
+    out = []
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            out.append(t)
+            continue
+        if t.get_device() != dev:
+            raise HQError(fn, 1)
+        out.append(t.data_ptr())
+    return out
+
+
+def hq_rope_table(rope, P, table, stream=None):
+    """Cosines and sines of P positions, fp32 [P, rope.rot_dim]."""
+    table, = _on_device("hq_rope_table", table)
+    _check("hq_rope_table", _lib().hq_rope_table(ctypes.byref(rope), P, table, _stream(stream)))
+
+
+def hq_rope(rope, T, H, D, x, x_token_stride, x_head_stride, positions, table, P, out, out_token_stride,
+            out_head_stride, stream=None):
+    """Rotates x [T, H, D] by the positions' rows of `table` into out (which may be x)."""
+    x, positions, table, out = _on_device("hq_rope", x, positions, table, out)
+    _check("hq_rope", _lib().hq_rope(
+        ctypes.byref(rope), T, H, D, x, x_token_stride, x_head_stride, positions, table, P, out, out_token_stride,
+        out_head_stride, _stream(stream)))
+
+
+def hq_kv_page_bytes(kv) -> int:
+    return _lib().hq_kv_page_bytes(ctypes.byref(kv))
+
+
+def hq_kv_write(kv, T, k, k_stride, v, v_stride, slots, global_scale, num_pages, pages, stream=None):
+    """Quantises T tokens' keys and values into their slots of the paged cache."""
+    k, v, slots, global_scale, pages = _on_device("hq_kv_write", k, v, slots, global_scale, pages)
+    _check("hq_kv_write", _lib().hq_kv_write(
+        ctypes.byref(kv), T, k, k_stride, v, v_stride, slots, global_scale, num_pages, pages, _stream(stream)))
+
+
+def hq_rope_kv_write(rope, kv, T, q_heads, q, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride, positions,
+                     table, P, slots, global_scale, num_pages, pages, stream=None):
+    """hq_kv_write with k (and q, into q_out) rotated, in one launch."""
+    q, q_out, k, v, positions, table, slots, global_scale, pages = _on_device(
+        "hq_rope_kv_write", q, q_out, k, v, positions, table, slots, global_scale, pages)
+    _check("hq_rope_kv_write", _lib().hq_rope_kv_write(
+        ctypes.byref(rope), ctypes.byref(kv), T, q_heads, q, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride,
+        positions, table, P, slots, global_scale, num_pages, pages, _stream(stream)))
+
+
+def hq_kv_read(kv, T, slots, global_scale, num_pages, pages, k_out, k_stride, v_out, v_stride, stream=None):
+    """Reads T slots of the paged cache back to bf16."""
+    slots, global_scale, pages, k_out, v_out = _on_device("hq_kv_read", slots, global_scale, pages, k_out, v_out)
+    _check("hq_kv_read", _lib().hq_kv_read(
+        ctypes.byref(kv), T, slots, global_scale, num_pages, pages, k_out, k_stride, v_out, v_stride,
+        _stream(stream)))
+
+
+def hq_paged_attn_workspace_bytes(kv, B, q_heads) -> int:
+    return _lib().hq_paged_attn_workspace_bytes(ctypes.byref(kv), B, q_heads)
+
+
+def hq_paged_attn(kv, B, q_heads, q, q_stride, global_scale, num_pages, pages, page_table, max_pages, lengths, scale,
+                  window, out, out_stride, lse, workspace, ws_bytes, stream=None):
+    """Attention of one new token per sequence over the paged cache."""
+    q, global_scale, pages, page_table, lengths, out, lse, workspace = _on_device(
+        "hq_paged_attn", q, global_scale, pages, page_table, lengths, out, lse, workspace)
+    _check("hq_paged_attn", _lib().hq_paged_attn(
+        ctypes.byref(kv), B, q_heads, q, q_stride, global_scale, num_pages, pages, page_table, max_pages, lengths,
+        scale, window, out, out_stride, lse, workspace, ws_bytes, _stream(stream)))

@@ -338,7 +338,7 @@ const char *hq_status_string(hq_status s) {
     case HQ_ERR_WORKSPACE: return "workspace too small";
     case HQ_ERR_CUDA: return "CUDA error";
     case HQ_ERR_TIMEOUT: return "device-side wait timed out";
-    case HQ_ERR_DEVICE_INDEX: return "expert id out of range";
+    case HQ_ERR_DEVICE_INDEX: return "index out of range on the device";
     case HQ_ERR_ARCH: return "device is not sm_100";
     default: return "unknown status";
   }
@@ -689,6 +689,197 @@ hq_status hq_moe_unpermute_sum(int T, int topk, int N, const void *y_bf16, const
   if (!device_is_sm100()) return HQ_ERR_ARCH;
   return launch_unpermute_sum(T, topk, N, y_bf16, inv_perm, topk_weights, routed_scale, out_bf16,
                               (cudaStream_t)stream);
+}
+
+// ---- decoder cache ----------------------------------------------------------
+
+static bool valid_rope(const hq_rope_desc *r, int D) {
+  return r->rot_dim >= 2 && r->rot_dim <= D && (r->rot_dim % 2) == 0 && (r->interleaved == 0 || r->interleaved == 1);
+}
+
+// A stride between rows of `width` elements: 16-byte steps that do not overlap
+// (0 rows or one row: any).
+static bool valid_stride(int64_t stride) { return stride >= 0 && (stride % 8) == 0; }
+
+static hq_status check_kv(const hq_kv_desc *kv, int *fmt) {
+  if (!kv) return HQ_ERR_INVALID_ARG;
+  for (int i = 0; i < 4; ++i)
+    if (kv->reserved[i] != 0) return HQ_ERR_INVALID_ARG;
+  if (kv->heads < 1 || kv->heads > 1024 || kv->page_size < 16 || kv->page_size > 4096 || (kv->page_size % 16) != 0)
+    return HQ_ERR_INVALID_ARG;
+  return kv_format(kv, fmt) ? HQ_OK : HQ_ERR_UNSUPPORTED;
+}
+
+// The cache's pointers, shared by every call on it.
+static hq_status check_pages(const hq_kv_desc *kv, int num_pages, const void *pages, const float *global_scale) {
+  if (num_pages < 1 || !pages || !aligned16(pages)) return HQ_ERR_INVALID_ARG;
+  return (kv->dtype == HQ_NVFP4) == (global_scale != nullptr) ? HQ_OK : HQ_ERR_INVALID_ARG;
+}
+
+hq_status hq_rope_table(const hq_rope_desc *rope, int P, float *table, hq_stream_t stream) {
+  if (!rope || !valid_rope(rope, 1024) || P < 0) return HQ_ERR_INVALID_ARG;
+  if (!(rope->base > 1.0) || !(rope->base < 1e30) || !(rope->amplitude >= 0.0)) return HQ_ERR_INVALID_ARG;
+  if (rope->scaling < HQ_ROPE_PLAIN || rope->scaling > HQ_ROPE_INDEX) return HQ_ERR_UNSUPPORTED;
+  if (rope->scaling != HQ_ROPE_PLAIN && !(rope->factor > 0.0)) return HQ_ERR_INVALID_ARG;
+  if (rope->scaling >= HQ_ROPE_TURNS && (!(rope->low > 0.0) || !(rope->high > rope->low) || rope->context < 1))
+    return HQ_ERR_INVALID_ARG;
+  if (P == 0) return HQ_OK;
+  if (!table || !aligned16(table)) return HQ_ERR_INVALID_ARG;
+  if (!device_is_sm100()) return HQ_ERR_ARCH;
+  return launch_rope_table(rope, P, table, (cudaStream_t)stream);
+}
+
+hq_status hq_rope(const hq_rope_desc *rope, int T, int H, int D, const void *x_bf16, int64_t x_token_stride,
+                  int64_t x_head_stride, const int32_t *positions, const float *table, int P, void *out_bf16,
+                  int64_t out_token_stride, int64_t out_head_stride, hq_stream_t stream) {
+  if (!rope || T < 0 || H < 1 || D < 8 || D > 1024 || (D % 8) != 0 || !valid_rope(rope, D) || P < 1)
+    return HQ_ERR_INVALID_ARG;
+  if (!valid_stride(x_token_stride) || !valid_stride(x_head_stride) || !valid_stride(out_token_stride) ||
+      !valid_stride(out_head_stride))
+    return HQ_ERR_INVALID_ARG;
+  if (T == 0) return HQ_OK;
+  if (!x_bf16 || !positions || !table || !out_bf16 || !aligned16(x_bf16) || !aligned16(table) || !aligned16(out_bf16))
+    return HQ_ERR_INVALID_ARG;
+  if (x_bf16 == out_bf16 && (x_token_stride != out_token_stride || x_head_stride != out_head_stride))
+    return HQ_ERR_INVALID_ARG;
+  if (!device_is_sm100()) return HQ_ERR_ARCH;
+  const RopeArgs a{T, H, D, rope->rot_dim, rope->interleaved, P, (const uint16_t *)x_bf16, x_token_stride,
+                   x_head_stride, positions, table, (uint16_t *)out_bf16, out_token_stride, out_head_stride};
+  return launch_rope(a, (cudaStream_t)stream);
+}
+
+size_t hq_kv_page_bytes(const hq_kv_desc *kv) {
+  int fmt;
+  return check_kv(kv, &fmt) == HQ_OK ? kv_page_bytes(kv, fmt) : 0;
+}
+
+static hq_status kv_write(const hq_rope_desc *rope, const hq_kv_desc *kv, int T, int q_heads, const void *q,
+                          int64_t q_stride, void *q_out, int64_t q_out_stride, const void *k, int64_t k_stride,
+                          const void *v, int64_t v_stride, const int32_t *positions, const float *table, int P,
+                          const int64_t *slots, const float *global_scale, int num_pages, void *pages,
+                          hq_stream_t stream) {
+  int fmt;
+  const hq_status s = check_kv(kv, &fmt);
+  if (s != HQ_OK) return s;
+  if (T < 0 || !valid_stride(k_stride) || !valid_stride(v_stride)) return HQ_ERR_INVALID_ARG;
+  if (rope) {
+    if (!valid_rope(rope, kv->head_dim) || P < 1 || q_heads < 0 || q_heads > 65536) return HQ_ERR_INVALID_ARG;
+    if (q_heads && (!valid_stride(q_stride) || !valid_stride(q_out_stride))) return HQ_ERR_INVALID_ARG;
+  }
+  if (T == 0) return HQ_OK;
+  if (!k || !v || !slots || !aligned16(k) || !aligned16(v)) return HQ_ERR_INVALID_ARG;
+  if (rope && (!positions || !table || !aligned16(table))) return HQ_ERR_INVALID_ARG;
+  if (q_heads ? (!q || !q_out || !aligned16(q) || !aligned16(q_out) || (q == q_out && q_stride != q_out_stride))
+              : (q || q_out))
+    return HQ_ERR_INVALID_ARG;
+  const hq_status ps = check_pages(kv, num_pages, pages, global_scale);
+  if (ps != HQ_OK) return ps;
+  if (!device_is_sm100()) return HQ_ERR_ARCH;
+  const int D = kv->head_dim;
+  const KvArgs a = kv_args(kv, fmt, num_pages, pages, global_scale);
+  KvRows w{};
+  w.T = T;
+  w.k = (const uint16_t *)k;
+  w.v = (const uint16_t *)v;
+  w.ks = k_stride;
+  w.vs = v_stride;
+  w.slots = (const long long *)slots;
+  RopeArgs r{};
+  if (rope) {
+    r = RopeArgs{T, q_heads, D, rope->rot_dim, rope->interleaved, P, (const uint16_t *)q, q_stride, D,
+                 positions, table, (uint16_t *)q_out, q_out_stride, D};
+  }
+  return launch_kv_write(fmt, D, a, w, r, (cudaStream_t)stream);
+}
+
+hq_status hq_kv_write(const hq_kv_desc *kv, int T, const void *k_bf16, int64_t k_stride, const void *v_bf16,
+                      int64_t v_stride, const int64_t *slots, const float *global_scale, int num_pages, void *pages,
+                      hq_stream_t stream) {
+  return kv_write(nullptr, kv, T, 0, nullptr, 0, nullptr, 0, k_bf16, k_stride, v_bf16, v_stride, nullptr, nullptr, 0,
+                  slots, global_scale, num_pages, pages, stream);
+}
+
+hq_status hq_rope_kv_write(const hq_rope_desc *rope, const hq_kv_desc *kv, int T, int q_heads, const void *q_bf16,
+                           int64_t q_stride, void *q_out_bf16, int64_t q_out_stride, const void *k_bf16,
+                           int64_t k_stride, const void *v_bf16, int64_t v_stride, const int32_t *positions,
+                           const float *table, int P, const int64_t *slots, const float *global_scale, int num_pages,
+                           void *pages, hq_stream_t stream) {
+  if (!rope) return HQ_ERR_INVALID_ARG;
+  return kv_write(rope, kv, T, q_heads, q_bf16, q_stride, q_out_bf16, q_out_stride, k_bf16, k_stride, v_bf16,
+                  v_stride, positions, table, P, slots, global_scale, num_pages, pages, stream);
+}
+
+hq_status hq_kv_read(const hq_kv_desc *kv, int T, const int64_t *slots, const float *global_scale, int num_pages,
+                     const void *pages, void *k_out_bf16, int64_t k_stride, void *v_out_bf16, int64_t v_stride,
+                     hq_stream_t stream) {
+  int fmt;
+  const hq_status s = check_kv(kv, &fmt);
+  if (s != HQ_OK) return s;
+  if (T < 0 || !valid_stride(k_stride) || !valid_stride(v_stride)) return HQ_ERR_INVALID_ARG;
+  if (T == 0) return HQ_OK;
+  if (!slots || (!k_out_bf16 && !v_out_bf16) || !aligned16(k_out_bf16) || !aligned16(v_out_bf16))
+    return HQ_ERR_INVALID_ARG;
+  const hq_status ps = check_pages(kv, num_pages, pages, global_scale);
+  if (ps != HQ_OK) return ps;
+  if (!device_is_sm100()) return HQ_ERR_ARCH;
+  const KvArgs a = kv_args(kv, fmt, num_pages, pages, global_scale);
+  KvRows w{};
+  w.T = T;
+  w.ks = k_stride;
+  w.vs = v_stride;
+  w.slots = (const long long *)slots;
+  w.k_out = (uint16_t *)k_out_bf16;
+  w.v_out = (uint16_t *)v_out_bf16;
+  return launch_kv_read(fmt, kv->head_dim, a, w, (cudaStream_t)stream);
+}
+
+static bool valid_q_heads(const hq_kv_desc *kv, int B, int q_heads) {
+  return B >= 0 && B <= (1 << 20) && q_heads >= kv->heads && q_heads <= 65536 && (q_heads % kv->heads) == 0;
+}
+
+size_t hq_paged_attn_workspace_bytes(const hq_kv_desc *kv, int B, int q_heads) {
+  int fmt;
+  if (check_kv(kv, &fmt) != HQ_OK || !valid_q_heads(kv, B, q_heads)) return 0;
+  return attn_workspace_bytes(fmt, kv->head_dim, q_heads / kv->heads, device_sm_count());
+}
+
+hq_status hq_paged_attn(const hq_kv_desc *kv, int B, int q_heads, const void *q_bf16, int64_t q_stride,
+                        const float *global_scale, int num_pages, const void *pages, const int32_t *page_table,
+                        int max_pages, const int32_t *lengths, float scale, int window, void *out_bf16,
+                        int64_t out_stride, float *lse, void *workspace, size_t ws_bytes, hq_stream_t stream) {
+  int fmt;
+  const hq_status s = check_kv(kv, &fmt);
+  if (s != HQ_OK) return s;
+  if (!valid_q_heads(kv, B, q_heads) || !valid_stride(q_stride) || !valid_stride(out_stride) || max_pages < 1 ||
+      (int64_t)max_pages * kv->page_size > INT32_MAX || window < 0)
+    return HQ_ERR_INVALID_ARG;
+  if (!(scale >= -3e38f && scale <= 3e38f)) return HQ_ERR_INVALID_ARG;
+  if (B == 0) return HQ_OK;
+  if (!q_bf16 || !page_table || !lengths || !out_bf16 || !aligned16(q_bf16) || !aligned16(out_bf16))
+    return HQ_ERR_INVALID_ARG;
+  const hq_status ps = check_pages(kv, num_pages, pages, global_scale);
+  if (ps != HQ_OK) return ps;
+  const int group = q_heads / kv->heads;
+  if (!workspace || !aligned16(workspace) ||
+      ws_bytes < attn_workspace_bytes(fmt, kv->head_dim, group, device_sm_count()))
+    return HQ_ERR_WORKSPACE;
+  if (!device_is_sm100()) return HQ_ERR_ARCH;
+  AttnArgs a{};
+  a.kv = kv_args(kv, fmt, num_pages, pages, global_scale);
+  a.B = B;
+  a.q_heads = q_heads;
+  a.group = group;
+  a.q = (const uint16_t *)q_bf16;
+  a.qs = q_stride;
+  a.page_table = page_table;
+  a.max_pages = max_pages;
+  a.lengths = lengths;
+  a.scale = scale * 1.4426950408889634f;
+  a.window = window;
+  a.out = (uint16_t *)out_bf16;
+  a.os = out_stride;
+  a.lse = lse;
+  return launch_attn(fmt, kv->head_dim, a, workspace, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -6,5 +6,7 @@
 #include "hq_gemm_small.cu"
 #include "hq_gemm_bs.cu"
 #include "hq_moe.cu"
+#include "hq_cache.cu"
+#include "hq_attn.cu"
 #include "hq_api.cu"
 #include "hq_noalloc.cu"

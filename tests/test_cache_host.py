@@ -1,0 +1,123 @@
+"""Host-side checks of the decoder-cache entry points (no GPU needed): page
+sizes, argument checks before any device work, and no-ops."""
+import ctypes
+
+import pytest
+
+import quantized_gemm_02_b200 as hq
+
+OK = hq.KVDesc(dtype=hq.HQ_E4M3, heads=8, head_dim=128, page_size=16)
+
+
+def kv(**kw):
+    d = dict(dtype=hq.HQ_E4M3, heads=8, head_dim=128, page_size=16)
+    d.update(kw)
+    return hq.KVDesc(**d)
+
+
+def refused(status, fn, *args):
+    with pytest.raises(hq.HQError) as e:
+        fn(*args, stream=0)
+    assert e.value.status == status, e.value
+
+
+@pytest.mark.parametrize("heads,D,page", [(1, 64, 16), (8, 128, 64), (3, 192, 48), (16, 256, 4096)])
+def test_page_bytes(heads, D, page):
+    rows = 2 * heads * page  # K and V of every head and token
+    assert hq.hq_kv_page_bytes(kv(dtype=hq.HQ_BF16, heads=heads, head_dim=D, page_size=page)) == rows * 2 * D
+    assert hq.hq_kv_page_bytes(kv(heads=heads, head_dim=D, page_size=page)) == rows * (D + 4)
+    assert hq.hq_kv_page_bytes(kv(dtype=hq.HQ_NVFP4, heads=heads, head_dim=D, page_size=page)) == rows * (D // 2 + D // 16)
+
+
+BAD = [dict(dtype=hq.HQ_MXFP8), dict(dtype=99), dict(heads=0), dict(heads=1025), dict(head_dim=96), dict(head_dim=0),
+       dict(page_size=0), dict(page_size=8), dict(page_size=24), dict(page_size=8192), dict(reserved=(ctypes.c_int32 * 4)(0, 1))]
+
+
+@pytest.mark.parametrize("bad", BAD, ids=lambda d: "-".join(d))
+def test_descriptions_that_are_refused(bad):
+    d = kv(**bad)
+    status = 2 if set(bad) & {"dtype", "head_dim"} else 1
+    assert hq.hq_kv_page_bytes(d) == 0
+    assert hq.hq_paged_attn_workspace_bytes(d, 1, 1024) == 0
+    refused(status, hq.hq_kv_write, d, 1, 16, 1024, 16, 1024, 16, None, 4, 16)
+    refused(status, hq.hq_kv_read, d, 1, 16, None, 4, 16, 16, 1024, 16, 1024)
+    refused(status, hq.hq_paged_attn, d, 1, 1024, 16, 8192, None, 4, 16, 16, 4, 16, 1.0, 0, 16, 8192, None, 16, 1 << 40)
+
+
+def test_table_arguments():
+    ok = dict(rot_dim=64, base=10000.0)
+    call = lambda P=4, t=16, **kw: refused(kw.pop("status", 1), hq.hq_rope_table, hq.RopeDesc(**dict(ok, **kw)), P, t)  # noqa: E731
+    for bad in (dict(rot_dim=0), dict(rot_dim=63), dict(rot_dim=1026), dict(base=1.0), dict(base=float("nan")), dict(base=float("inf")),
+                dict(amplitude=-1.0), dict(amplitude=float("nan")), dict(interleaved=2), dict(scaling=1), dict(scaling=1, factor=float("nan")),
+                dict(scaling=2, factor=2.0, context=4, low=1.0, high=1.0), dict(scaling=2, factor=2.0, low=1.0, high=4.0),
+                dict(scaling=3, factor=2.0, context=4, low=0.0, high=1.0), dict(scaling=3, factor=-2.0, context=4, low=1.0, high=2.0)):
+        call(**bad)
+    call(status=2, scaling=4, factor=2.0)
+    call(P=-1)
+    call(t=None)
+    call(t=20)
+    hq.hq_rope_table(hq.RopeDesc(**ok), 0, None, stream=0)
+
+
+def test_rope_arguments():
+    good = dict(T=2, H=2, D=64, x=16, xt=128, xh=64, pos=16, table=16, P=8, out=32, ot=128, oh=64)
+
+    def call(rope=hq.RopeDesc(rot_dim=64), **kw):
+        a = dict(good, **kw)
+        hq.hq_rope(rope, a["T"], a["H"], a["D"], a["x"], a["xt"], a["xh"], a["pos"], a["table"], a["P"], a["out"],
+                   a["ot"], a["oh"], stream=0)
+
+    for bad in (dict(T=-1), dict(H=0), dict(D=60), dict(D=1032), dict(D=0), dict(x=24), dict(x=None), dict(pos=None), dict(table=None),
+                dict(table=20), dict(P=0), dict(out=None), dict(out=40), dict(xt=127), dict(xh=-64), dict(ot=4), dict(oh=12),
+                dict(rope=hq.RopeDesc(rot_dim=66)), dict(rope=hq.RopeDesc(rot_dim=7)), dict(rope=hq.RopeDesc(rot_dim=64, interleaved=3)),
+                dict(out=16, ot=256)):
+        with pytest.raises(hq.HQError) as e:
+            call(**bad)
+        assert e.value.status == 1, bad
+    call(T=0, x=None, out=None)
+
+
+def test_write_and_read_arguments():
+    w = lambda d=OK, T=1, k=16, ks=1024, v=16, vs=1024, slots=16, g=None, n=4, pages=16: (d, T, k, ks, v, vs, slots, g, n, pages)  # noqa: E731
+    for bad in (dict(T=-1), dict(k=None), dict(v=None), dict(k=8), dict(v=24), dict(ks=1020), dict(vs=-8), dict(slots=None), dict(n=0),
+                dict(pages=None), dict(pages=8), dict(g=16), dict(d=kv(dtype=hq.HQ_NVFP4))):
+        refused(1, hq.hq_kv_write, *w(**bad))
+    hq.hq_kv_write(*w(T=0, k=None, v=None, slots=None, pages=None), stream=0)
+    r = lambda d=OK, T=1, slots=16, g=None, n=4, pages=16, k=16, ks=1024, v=16, vs=1024: (d, T, slots, g, n, pages, k, ks, v, vs)  # noqa: E731
+    for bad in (dict(T=-1), dict(slots=None), dict(k=None, v=None), dict(k=8), dict(v=8), dict(ks=4), dict(vs=-8), dict(n=0),
+                dict(pages=None), dict(g=16), dict(d=kv(dtype=hq.HQ_NVFP4))):
+        refused(1, hq.hq_kv_read, *r(**bad))
+    hq.hq_kv_read(*r(T=0, slots=None, pages=None, k=None, v=None), stream=0)
+
+
+def test_rope_write_arguments():
+    rope = hq.RopeDesc(rot_dim=128)
+    names = ["rope", "kv", "T", "Hq", "q", "qs", "qo", "qos", "k", "ks", "v", "vs", "pos", "table", "P", "slots", "g", "n", "pages"]
+    good = dict(zip(names, [rope, OK, 1, 8, 16, 1024, 16, 1024, 16, 1024, 16, 1024, 16, 16, 4, 16, None, 4, 16]))
+    for bad in (dict(rope=hq.RopeDesc(rot_dim=130)), dict(rope=hq.RopeDesc(rot_dim=0)), dict(Hq=-1), dict(q=None), dict(qo=None),
+                dict(q=8), dict(qs=4), dict(qos=-8), dict(qos=2048), dict(pos=None), dict(table=None), dict(table=20), dict(P=0),
+                dict(Hq=0), dict(k=None), dict(slots=None), dict(pages=None)):
+        refused(1, hq.hq_rope_kv_write, *dict(good, **bad).values())
+    hq.hq_rope_kv_write(*dict(good, T=0).values(), stream=0)
+
+
+def test_attention_arguments():
+    names = ["kv", "B", "Hq", "q", "qs", "g", "n", "pages", "pt", "most", "lens", "scale", "window", "out", "os", "lse", "ws", "wsb"]
+    need = hq.hq_paged_attn_workspace_bytes(OK, 4, 32)
+    assert need > 0
+    good = dict(zip(names, [OK, 4, 32, 16, 4096, None, 9, 16, 16, 7, 16, 0.1, 0, 16, 4096, None, 16, need]))
+    for bad in (dict(B=-1), dict(B=1 << 21), dict(Hq=0), dict(Hq=4), dict(Hq=33), dict(q=None), dict(q=8), dict(qs=4), dict(g=16), dict(n=0),
+                dict(pages=None), dict(pages=8), dict(pt=None), dict(most=0), dict(most=1 << 28), dict(lens=None), dict(scale=float("nan")),
+                dict(scale=float("inf")), dict(window=-1), dict(out=None), dict(out=8), dict(os=-8), dict(os=12),
+                dict(kv=kv(dtype=hq.HQ_NVFP4))):
+        refused(1, hq.hq_paged_attn, *dict(good, **bad).values())
+    for bad in (dict(ws=None), dict(ws=8), dict(wsb=need - 1)):
+        refused(3, hq.hq_paged_attn, *dict(good, **bad).values())
+    hq.hq_paged_attn(*dict(good, B=0, q=None, pt=None, lens=None, out=None, ws=None).values(), stream=0)
+    assert hq.hq_paged_attn_workspace_bytes(OK, 4, 33) == 0
+
+
+def test_tensors_that_are_not_on_the_device_are_refused():
+    import torch
+    t = torch.zeros(4, 64)
+    refused(1, hq.hq_rope_table, hq.RopeDesc(rot_dim=64, base=10000.0), 4, t)
