@@ -840,7 +840,7 @@ static bool valid_q_heads(const hq_kv_desc *kv, int B, int q_heads) {
 size_t hq_paged_attn_workspace_bytes(const hq_kv_desc *kv, int B, int q_heads) {
   int fmt;
   if (check_kv(kv, &fmt) != HQ_OK || !valid_q_heads(kv, B, q_heads)) return 0;
-  return attn_workspace_bytes(fmt, kv->head_dim, q_heads / kv->heads, device_sm_count());
+  return attn_workspace_bytes(kv->head_dim, q_heads / kv->heads, device_sm_count());
 }
 
 hq_status hq_paged_attn(const hq_kv_desc *kv, int B, int q_heads, const void *q_bf16, int64_t q_stride,
@@ -860,12 +860,13 @@ hq_status hq_paged_attn(const hq_kv_desc *kv, int B, int q_heads, const void *q_
   const hq_status ps = check_pages(kv, num_pages, pages, global_scale);
   if (ps != HQ_OK) return ps;
   const int group = q_heads / kv->heads;
-  if (!workspace || !aligned16(workspace) ||
-      ws_bytes < attn_workspace_bytes(fmt, kv->head_dim, group, device_sm_count()))
+  const int sms = device_sm_count();
+  if (!workspace || !aligned16(workspace) || ws_bytes < attn_workspace_bytes(kv->head_dim, group, sms))
     return HQ_ERR_WORKSPACE;
   if (!device_is_sm100()) return HQ_ERR_ARCH;
   AttnArgs a{};
   a.kv = kv_args(kv, fmt, num_pages, pages, global_scale);
+  a.num_pages = num_pages;
   a.B = B;
   a.q_heads = q_heads;
   a.group = group;
@@ -879,7 +880,7 @@ hq_status hq_paged_attn(const hq_kv_desc *kv, int B, int q_heads, const void *q_
   a.out = (uint16_t *)out_bf16;
   a.os = out_stride;
   a.lse = lse;
-  return launch_attn(fmt, kv->head_dim, a, workspace, (cudaStream_t)stream);
+  return launch_attn(fmt, kv->head_dim, a, sms, workspace, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -1,5 +1,41 @@
 // Attention of one new token per sequence over the paged key-value cache.
+//
+// The operation reads each cached key and value once and does 4 G D flops per
+// token and kv head with them (G query heads share a kv head): 1 to 16 flops
+// a byte, far under what the tensor cores need, so HBM bounds it and the
+// kernel is built around the stream of cache units (16 tokens of one head,
+// contiguous, see hq_cache.cu):
+//
+//   * The units of all sequences and kv heads form one line, cut into equal
+//     parts for the SMs and, inside an SM, for its warps; ragged lengths
+//     therefore balance to one unit, and lengths are read on the device (a
+//     captured call serves growing sequences).  A warp streams its units
+//     through a private ring with one bulk copy each; warps meet only at the
+//     end.
+//   * Tokens are the M side of m16n8k16 MMAs and the query heads the N side:
+//     S^T = K Q^T, O^T = V^T P^T.  Eight heads fill N, no row of the MMA is
+//     padding, and every cache byte is read by exactly one lane, so the cache
+//     is stored in fragment order and converted in registers on the way (no
+//     transposition, no second pass through shared memory).  The tcgen05 path
+//     would need the converted tile written back to shared or tensor memory,
+//     and 128 tokens per tile, for an MMA that is idle anyway.
+//   * Softmax in base 2 with a running reference per head; the reference only
+//     moves when a score exceeds it by 2^LIM, so most units need no exchange
+//     between lanes.
+//   * Parts of an item (a sequence's kv head) are joined by their log sums:
+//     warps of a CTA through shared memory, CTAs through the workspace by the
+//     last one to arrive, always in the order of the tokens.
+//
+// Arithmetic.  Scores and sums are fp32.  bf16 caches multiply in bf16 with
+// each weight split into two bf16 numbers (hi + lo, 2^-17 of the weight);
+// E4M3 and NVFP4 codes (and code times block scale) are exact in fp16, so
+// those caches multiply in fp16, with q scaled by a power of two per head into
+// fp16's range (exact down to 2^-39 of the head's largest) and weights rounded
+// to fp16 (2^-11) around a reference of 2^10.  E4M3 values carry an fp32 scale
+// per token: it multiplies the weight, and those products have a reference of
+// their own, so that any range of scales keeps the weight's precision.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "hq_internal.cuh"
 
@@ -7,7 +43,9 @@ namespace hq {
 
 struct AttnArgs {
   KvArgs kv;
+  int num_pages;
   int B, q_heads, group;       // query heads per kv head
+  int hgroups;                 // groups of GT query heads per kv head
   const uint16_t *q;
   long long qs;                // stride between sequences, elements
   const int32_t *page_table;
@@ -18,94 +56,752 @@ struct AttnArgs {
   uint16_t *out;
   long long os;
   float *lse;
+  int *counters;               // [CTAs]
+  float *parts;                // [CTAs][2] partial records
 };
 
 // The tokens a sequence's query sees: [first, len).
 __device__ __forceinline__ int attn_range(const AttnArgs &a, int b, int &first) {
   int n = a.lengths[b];
-  const long long most = (long long)a.max_pages * a.kv.page;
+  const int most = a.max_pages * a.kv.page;
   if (n < 0 || n > most) {
     set_device_error(HQ_ERR_DEVICE_INDEX);
-    n = n < 0 ? 0 : (int)most;
+    n = n < 0 ? 0 : most;
   }
   first = a.window > 0 && n > a.window ? n - a.window : 0;
   return n;
 }
-
-// One CTA per (sequence, query head): 128 tokens at a time, one score per
-// thread, then the channels summed over the 128 weights.
-template <int FMT, int D>
-__global__ void __launch_bounds__(128) attn_kernel(AttnArgs a) {
-  __shared__ float sq[D], sp[128], red[4];
-  __shared__ const uint8_t *su[128];
-  const int b = blockIdx.x / a.q_heads, hq = blockIdx.x % a.q_heads, h = hq / a.group, tid = threadIdx.x;
+__device__ __forceinline__ int attn_units(const AttnArgs &a, int b) {
   int first;
   const int n = attn_range(a, b, first);
-  for (int d = tid; d < D; d += 128) sq[d] = bf16_at(a.q + b * a.qs + (size_t)hq * D + d) * a.scale;
-  float m = -INFINITY, l = 0.f, acc[(D + 127) / 128];
-  for (auto &x : acc) x = 0.f;
-  for (int base = first; base < n; base += 128) {
-    const int j = base + tid;
-    float s = -INFINITY;
-    const uint8_t *unit = nullptr;
-    int r = 0;
-    if (j < n) {
-      const int pg = a.page_table[(size_t)b * a.max_pages + j / a.kv.page];
-      if (pg < 0 || (long long)pg * a.kv.page >= a.kv.slots_total) {
-        set_device_error(HQ_ERR_DEVICE_INDEX);
-      } else {
-        unit = kv_unit<FMT, D>(a.kv, (long long)pg * a.kv.page + j % a.kv.page, h, r);
-      }
-    }
-    __syncthreads();
-    if (unit) {
-      s = 0.f;
-      for (int o = 0; o < D / 8; ++o) {
-        float f[8];
-        kv_load<FMT, D>(unit, r, o, false, a.kv.glob, f);
-        for (int i = 0; i < 8; ++i) s += f[i] * sq[8 * o + i];
-      }
-    }
-    float mx = s;
-    for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-    if ((tid & 31) == 0) red[tid >> 5] = mx;
-    su[tid] = unit;
-    __syncthreads();
-    mx = fmaxf(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])), m);
-    const float ref = mx == -INFINITY ? 0.f : mx;
-    const float keep = exp2f(m - ref), p = exp2f(s - ref);
-    m = mx;
-    sp[tid] = p;
-    l = l * keep + p;
-    __syncthreads();
-    for (int c = 0; c * 128 + tid < D; ++c) {
-      const int d = c * 128 + tid;
-      float x = acc[c] * keep;
-      for (int i = 0; i < 128; ++i) {
-        if (!su[i]) continue;
-        float f[8];
-        kv_load<FMT, D>(su[i], (base + i) % 16, d >> 3, true, a.kv.glob, f);
-        x += sp[i] * f[d & 7];
-      }
-      acc[c] = x;
-    }
-  }
-  for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-  __syncthreads();
-  if ((tid & 31) == 0) red[tid >> 5] = l;
-  __syncthreads();
-  l = red[0] + red[1] + red[2] + red[3];
-  for (int c = 0; c * 128 + tid < D; ++c)
-    a.out[b * a.os + (size_t)hq * D + c * 128 + tid] = to_bf16(l > 0.f ? acc[c] / l : 0.f);
-  if (tid == 0 && a.lse) a.lse[(size_t)b * a.q_heads + hq] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  return n ? (int)(((long long)n + 15) / 16) - first / 16 : 0;
 }
 
-size_t attn_workspace_bytes(int, int, int, int) { return 256; }
+// ---- fragments ---------------------------------------------------------------
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)c));
+  return r;
+}
+template <int I>
+__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t w) {  // byte I of w
+  uint32_t r;
+  if constexpr (I == 0) asm("{.reg .b8 a,b,c,d; mov.b32 {a,b,c,d}, %1; cvt.rn.f16x2.e2m1x2 %0, a;}" : "=r"(r) : "r"(w));
+  if constexpr (I == 1) asm("{.reg .b8 a,b,c,d; mov.b32 {a,b,c,d}, %1; cvt.rn.f16x2.e2m1x2 %0, b;}" : "=r"(r) : "r"(w));
+  if constexpr (I == 2) asm("{.reg .b8 a,b,c,d; mov.b32 {a,b,c,d}, %1; cvt.rn.f16x2.e2m1x2 %0, c;}" : "=r"(r) : "r"(w));
+  if constexpr (I == 3) asm("{.reg .b8 a,b,c,d; mov.b32 {a,b,c,d}, %1; cvt.rn.f16x2.e2m1x2 %0, d;}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// 8 x 8 transposition of 16-bit values held as MMA fragments.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+template <bool BF>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (BF)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
-hq_status launch_attn(int fmt, int D, const AttnArgs &a, void *, cudaStream_t st) {
+// ---- shape of a kernel ---------------------------------------------------------
+// NT = 8-head tiles per item.  W warps, each with a ring of STAGES units.  A
+// partial record is GT x D normalised outputs and GT log2 sums; a warp keeps
+// at most two, one of them in its drained ring.
+constexpr int ATTN_SMEM = 227 * 1024 - 512;  // what a CTA may have, less the static part
+constexpr int ATTN_HEAD = 1280;              // barriers and bookkeeping
+template <int FMT, int D, int NT>
+struct AttnShape {
+  static constexpr int GT = 8 * NT;
+  static constexpr int UNIT = kv_unit_bytes(FMT, D);
+  static constexpr int PART = GT * (D + 4) * 4;  // bytes; the sums padded to 16 per head
+  static constexpr int fit(int w) { return ((ATTN_SMEM - ATTN_HEAD) / w - PART) / UNIT; }
+  static constexpr int W = fit(8) >= 3 ? 8 : 4;
+  static constexpr int STAGES = fit(W) < 12 ? fit(W) : 12;
+  static constexpr int SMEM = ATTN_HEAD + W * (PART + STAGES * UNIT);
+  static_assert(STAGES >= 2 && STAGES * UNIT >= PART, "ring too small");
+};
+
+struct AttnSeg {         // a part of an item that a warp leaves behind
+  long long start;       // the item's first unit in the line
+  int b, it, nu;         // sequence, head group, units of the item
+  int flags;             // 1: present, 2: holds the item's first unit, 4: its last
+};
+
+struct AttnHead {
+  uint64_t full[96];     // [W][STAGES]
+  AttnSeg seg[16];       // [W][2]
+};
+struct AttnStart {
+  long long off[8];
+  int b[8];
+};
+
+// A walk along the line of units.
+struct AttnWalk {
+  int b, it, u, nu, u0, len, first;
+  __device__ __forceinline__ void open(const AttnArgs &a) {
+    len = attn_range(a, b, first);
+    u0 = first / 16;
+    nu = len ? (int)(((long long)len + 15) / 16) - u0 : 0;
+  }
+  // to the next unit; there is one
+  __device__ __forceinline__ bool next(const AttnArgs &a, int items) {
+    if (++u < nu) return false;
+    u = 0;
+    if (++it < items) return true;
+    it = 0;
+    do {
+      ++b;
+      open(a);
+    } while (nu == 0 && b < a.B - 1);
+    return true;
+  }
+};
+
+__device__ __forceinline__ int attn_cta_of(long long u, long long total, int ctas) {
+  return (int)(((u + 1) * ctas - 1) / total);
+}
+
+template <int FMT, int D, int NT>
+__global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32, 1) attn_kernel(AttnArgs a) {
+  using S = AttnShape<FMT, D, NT>;
+  constexpr int W = S::W, STAGES = S::STAGES, UNIT = S::UNIT, GT = S::GT, PART = S::PART;
+  constexpr int CB = kv_code_bytes(FMT, D), SB = kv_scale_bytes(FMT, D);
+  constexpr bool BF = FMT == A_BF16;
+  constexpr float LIM = BF ? 8.f : 15.f, SHIFT = BF ? 0.f : 10.f;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ long long s_scan[W + 1];
+  __shared__ AttnStart s_start;
+  __shared__ int s_last[2];
+  AttnHead *head = reinterpret_cast<AttnHead *>(smem);
+  static_assert(sizeof(AttnHead) <= ATTN_HEAD && W * STAGES <= 96, "bookkeeping");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  uint8_t *ring = smem + ATTN_HEAD + warp * (STAGES * UNIT);
+  float *rec0 = reinterpret_cast<float *>(smem + ATTN_HEAD + W * STAGES * UNIT) + warp * (PART / 4);
+  uint64_t *full = head->full + warp * STAGES;
+  const int items = a.kv.H * a.hgroups;
+
+  if (lane == 0) {
+    for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1);
+    head->seg[2 * warp].flags = head->seg[2 * warp + 1].flags = 0;
+    fence_barrier_init();
+  }
+
+  // empty sequences: zeros, written by whoever comes by
+  for (int b0 = (blockIdx.x * W + warp) * 32; b0 < a.B; b0 += gridDim.x * W * 32) {
+    unsigned empty = __ballot_sync(0xffffffffu, b0 + lane < a.B && attn_units(a, min(b0 + lane, a.B - 1)) == 0);
+    while (empty) {
+      const int b = b0 + __ffs(empty) - 1;
+      empty &= empty - 1;
+      for (int i = lane; i < a.q_heads * (D / 8); i += 32)
+        *reinterpret_cast<uint4 *>(a.out + b * a.os + (size_t)i * 8) = make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (int i = lane; i < a.q_heads; i += 32) a.lse[(size_t)b * a.q_heads + i] = -INFINITY;
+    }
+  }
+
+  // the line's length, and where each of this CTA's warps starts
+  const int per = (a.B + W * 32 - 1) / (W * 32);
+  const int bs = min(tid * per, a.B), be = min(bs + per, a.B);
+  long long mine = 0;
+  for (int b = bs; b < be; ++b) mine += attn_units(a, b);
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, sum = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w < warp) before += s_scan[w];
+    sum += s_scan[w];
+  }
+  const long long total = sum * items;
+  const long long want = (total + W - 1) / W;  // a unit per warp at least
+  const int ctas = (int)(want < gridDim.x ? want : gridDim.x);
+  if ((int)blockIdx.x >= ctas) return;
+  const long long c_begin = blockIdx.x * total / ctas, c_units = (blockIdx.x + 1) * total / ctas - c_begin;
+  if (mine) {
+    for (int w = 0; w < W; ++w) {
+      const long long at = c_begin + w * c_units / W;
+      if (at < before * items || at >= (before + mine) * items) continue;
+      long long p = before * items;
+      int b = bs;
+      while (true) {
+        const long long n = (long long)attn_units(a, b) * items;
+        if (at < p + n) break;
+        p += n;
+        ++b;
+      }
+      s_start.b[w] = b;
+      s_start.off[w] = at - p;
+    }
+  }
+  __syncthreads();
+
+  long long pos = c_begin + warp * c_units / W;  // the next unit to compute, along the line
+  int left = (int)(c_begin + (warp + 1) * c_units / W - pos);
+  if (left > 0) {
+    AttnWalk cw;  // what is computed
+    cw.b = s_start.b[warp];
+    cw.open(a);
+    cw.it = (int)(s_start.off[warp] / cw.nu);
+    cw.u = (int)(s_start.off[warp] % cw.nu);
+    AttnWalk pw = cw;  // what is fetched
+    const int upp = a.kv.page_units;
+    int pidx = (pw.u0 + pw.u) / upp, psub = (pw.u0 + pw.u) % upp;
+    int cache_b = -1, cache_at = 0, cached = 0;
+    int to_issue = left;
+    unsigned bad = 0;  // stages whose page does not exist
+
+    auto issue = [&](int stage) {
+      if (pw.b != cache_b || pidx < cache_at || pidx >= cache_at + 32) {
+        cache_b = pw.b;
+        cache_at = pidx;
+        // only pages the sequence reaches are read
+        cached = pidx + lane < (pw.len + a.kv.page - 1) / a.kv.page
+                     ? a.page_table[(size_t)pw.b * a.max_pages + pidx + lane] : 0;
+      }
+      const int pg = __shfl_sync(0xffffffffu, cached, pidx - cache_at);
+      const bool ok = pg >= 0 && pg < a.num_pages;
+      bad = ok ? bad & ~(1u << stage) : bad | (1u << stage);
+      if (lane == 0) {
+        if (ok) {
+          const uint8_t *src = a.kv.pages + (size_t)pg * a.kv.page_bytes +
+                               ((size_t)(pw.it / a.hgroups) * upp + psub) * UNIT;
+          mbar_arrive_expect_tx(&full[stage], UNIT);
+          bulk_g2s(ring + stage * UNIT, src, UNIT, &full[stage]);
+        } else {
+          set_device_error(HQ_ERR_DEVICE_INDEX);
+          mbar_arrive(&full[stage]);
+        }
+      }
+      if (--to_issue > 0) {
+        if (pw.next(a, items)) {
+          pidx = (pw.u0 + pw.u) / upp;
+          psub = (pw.u0 + pw.u) % upp;
+        } else if (++psub == upp) {
+          psub = 0;
+          ++pidx;
+        }
+      }
+    };
+    for (int s = 0; s < STAGES && to_issue > 0; ++s) issue(s);
+
+    uint32_t qf[NT][D / 16][2];  // B fragments of q: k = this lane's channels, n = head g
+    float qc[NT][2];             // score multiplier of heads 2t, 2t + 1
+    float o[NT][D / 16][4], l[NT][2], ref[NT][2], refv[NT][2];
+    bool fresh = true, alive = true;
+    int stage = 0;
+    uint32_t parity = 0;
+
+    while (left > 0) {
+      if (fresh) {
+        fresh = false;
+        const int h = cw.it / a.hgroups, hg = cw.it % a.hgroups;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int hq = hg * GT + nt * 8 + g;
+          const bool on = hq < a.group;
+          const uint16_t *src = a.q + cw.b * a.qs + (size_t)(h * a.group + (on ? hq : 0)) * D + 8 * t;
+          uint4 v[D / 32];
+          float amax = 0.f;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            v[i] = on ? *reinterpret_cast<const uint4 *>(src + 32 * i) : make_uint4(0, 0, 0, 0);
+            if constexpr (!BF) {
+              float f[8];
+              unpack8(v[i], f);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
+            }
+          }
+          float mult = 1.f, sc = a.scale;
+          if constexpr (!BF) {
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            const int ex = (int)(__float_as_uint(amax) >> 23);
+            // the head's largest |q| into [2^13, 2^14)
+            const int e = (amax == 0.f || ex == 255) ? 0 : max(ex - 140, -126);
+            mult = exp2i(-e);
+            sc *= exp2i(e);
+            if constexpr (FMT == A_NVFP4) sc *= a.kv.glob[0];
+          }
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            if constexpr (BF) {
+              qf[nt][2 * i][0] = v[i].x;
+              qf[nt][2 * i][1] = v[i].y;
+              qf[nt][2 * i + 1][0] = v[i].z;
+              qf[nt][2 * i + 1][1] = v[i].w;
+            } else {
+              float f[8];
+              unpack8(v[i], f);
+              qf[nt][2 * i][0] = f16x2(f[0] * mult, f[1] * mult);
+              qf[nt][2 * i][1] = f16x2(f[2] * mult, f[3] * mult);
+              qf[nt][2 * i + 1][0] = f16x2(f[4] * mult, f[5] * mult);
+              qf[nt][2 * i + 1][1] = f16x2(f[6] * mult, f[7] * mult);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            qc[nt][j] = __shfl_sync(0xffffffffu, sc, (2 * t + j) * 4);
+            l[nt][j] = 0.f;
+            ref[nt][j] = refv[nt][j] = -3e38f;
+          }
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
+        }
+      }
+
+      // a wait that gave up (recorded) ends the warp's copies; those in flight are waited for once, below
+      if (alive) alive = __all_sync(0xffffffffu, mbar_wait(&full[stage], parity));
+      if (alive && !(bad >> stage & 1u)) {
+        uint8_t *unit = ring + stage * UNIT;
+        const uint4 *kv4 = reinterpret_cast<const uint4 *>(unit) + lane;
+        const uint4 *vv4 = reinterpret_cast<const uint4 *>(unit + CB) + lane;
+        const uint8_t *ksc = unit + 2 * CB, *vsc = ksc + SB;
+        const int tok0 = (cw.u0 + cw.u) * 16;
+        const int lo = cw.first - tok0, hi = cw.len - tok0;  // valid tokens: [lo, hi) of 0..15
+        const bool edge = lo > 0 || hi < 16;
+        if (edge) {
+          // what lies past the sequence may be NaN, and 0 * NaN is: zero the values this lane reads
+          auto valid = [&](int tk) {  // token of the lane's value octets
+            const int j = 2 * t + (tk & 1) + 8 * (tk >> 1);
+            return j >= lo && j < hi;
+          };
+          constexpr int GS = kv_granule(FMT);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            if (valid(i & 3)) continue;
+            uint8_t *p = unit + CB + lane_byte<GS>(lane, i);
+            if constexpr (FMT == A_BF16) *reinterpret_cast<uint4 *>(p) = make_uint4(0, 0, 0, 0);
+            if constexpr (FMT == A_FP8) *reinterpret_cast<uint2 *>(p) = make_uint2(0, 0);
+            if constexpr (FMT == A_NVFP4) *reinterpret_cast<uint32_t *>(p) = 0;
+          }
+          if constexpr (FMT == A_NVFP4) {
+            for (int i = lane; i < D; i += 32)
+              if ((i & 15) < lo || (i & 15) >= hi) unit[2 * CB + SB + i] = 0;
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+
+        // S^T: rows g and g + 8 (tokens) x heads 2t, 2t + 1
+        float acc[NT][2][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[nt][0][j] = acc[nt][1][j] = 0.f;
+        auto qk = [&](int step, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816<BF>(acc[nt][step & 1], a0, a1, a2, a3, qf[nt][step][0], qf[nt][step][1]);
+        };
+        float kscale[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
+        if constexpr (FMT == A_BF16) {
+#pragma unroll
+          for (int b = 0; b < D / 32; ++b) {
+            const uint4 v0 = kv4[(2 * b) * 32], v1 = kv4[(2 * b + 1) * 32];
+            qk(2 * b, v0.x, v1.x, v0.y, v1.y);
+            qk(2 * b + 1, v0.z, v1.z, v0.w, v1.w);
+          }
+        } else if constexpr (FMT == A_FP8) {
+          kscale[0] = reinterpret_cast<const float *>(ksc)[g];
+          kscale[1] = reinterpret_cast<const float *>(ksc)[g + 8];
+          lv[0] = lg2(reinterpret_cast<const float *>(vsc)[g]);
+          lv[1] = lg2(reinterpret_cast<const float *>(vsc)[g + 8]);
+#pragma unroll
+          for (int b = 0; b < D / 32; ++b) {
+            const uint4 v = kv4[b * 32];
+            qk(2 * b, e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.z >> 16));
+            qk(2 * b + 1, e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.y >> 16),
+               e4m3x2_to_f16x2(v.w >> 16));
+          }
+        } else {
+          // this lane's channels 32b + 8t.. lie in 16-channel block 2b + t / 2
+          const uint16_t *s0 = reinterpret_cast<const uint16_t *>(ksc + g * (D / 16) + (t >> 1) * (D / 32));
+          const uint16_t *s1 = reinterpret_cast<const uint16_t *>(ksc + (g + 8) * (D / 16) + (t >> 1) * (D / 32));
+#pragma unroll
+          for (int b2 = 0; b2 < D / 64; ++b2) {
+            const uint4 v = kv4[b2 * 32];
+            const uint32_t p0 = e4m3x2_to_f16x2(s0[b2]), p1 = e4m3x2_to_f16x2(s1[b2]);
+            const uint32_t r0 = __byte_perm(p0, 0, 0x1010), r1 = __byte_perm(p1, 0, 0x1010);
+            const uint32_t t0 = __byte_perm(p0, 0, 0x3232), t1 = __byte_perm(p1, 0, 0x3232);
+            qk(4 * b2, hmul2(e2m1x2_to_f16x2<0>(v.x), r0), hmul2(e2m1x2_to_f16x2<0>(v.y), r1),
+               hmul2(e2m1x2_to_f16x2<1>(v.x), r0), hmul2(e2m1x2_to_f16x2<1>(v.y), r1));
+            qk(4 * b2 + 1, hmul2(e2m1x2_to_f16x2<2>(v.x), r0), hmul2(e2m1x2_to_f16x2<2>(v.y), r1),
+               hmul2(e2m1x2_to_f16x2<3>(v.x), r0), hmul2(e2m1x2_to_f16x2<3>(v.y), r1));
+            qk(4 * b2 + 2, hmul2(e2m1x2_to_f16x2<0>(v.z), t0), hmul2(e2m1x2_to_f16x2<0>(v.w), t1),
+               hmul2(e2m1x2_to_f16x2<1>(v.z), t0), hmul2(e2m1x2_to_f16x2<1>(v.w), t1));
+            qk(4 * b2 + 3, hmul2(e2m1x2_to_f16x2<2>(v.z), t0), hmul2(e2m1x2_to_f16x2<2>(v.w), t1),
+               hmul2(e2m1x2_to_f16x2<3>(v.z), t0), hmul2(e2m1x2_to_f16x2<3>(v.w), t1));
+          }
+        }
+
+        // softmax weights.  x: scores, y: scores + log2 of the value's scale (E4M3)
+        float x[NT][4], y[NT][4];
+        bool raise = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float s = (acc[nt][0][j] + acc[nt][1][j]) * qc[nt][j & 1];
+            if constexpr (FMT == A_FP8) s *= kscale[j >> 1];
+            float sv = s + lv[j >> 1];
+            if (edge) {
+              const int tk = g + 8 * (j >> 1);
+              if (tk < lo || tk >= hi) s = sv = -INFINITY;
+            }
+            x[nt][j] = s;
+            y[nt][j] = sv;
+            if constexpr (FMT == A_FP8) raise |= s > ref[nt][j & 1] + 64.f || sv > refv[nt][j & 1] + LIM;
+            else raise |= s > ref[nt][j & 1] + LIM;
+          }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float mx = fmaxf(x[nt][j], x[nt][2 + j]), mv = fmaxf(y[nt][j], y[nt][2 + j]);
+#pragma unroll
+              for (int k = 4; k < 32; k <<= 1) {
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+                if constexpr (FMT == A_FP8) mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, k));
+              }
+              const float r = fmaxf(ref[nt][j], mx - (FMT == A_FP8 ? 0.f : SHIFT));
+              const float keep = ex2(ref[nt][j] - r);
+              ref[nt][j] = r;
+              l[nt][j] *= keep;
+              float ko = keep;
+              if constexpr (FMT == A_FP8) {
+                const float rv = fmaxf(refv[nt][j], mv - SHIFT);
+                ko = ex2(refv[nt][j] - rv);
+                refv[nt][j] = rv;
+              }
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                o[nt][i][j] *= ko;
+                o[nt][i][2 + j] *= ko;
+              }
+            }
+        }
+        uint32_t pb[NT][2], pl[NT][2];  // B fragments of P^T: tokens 2t, 2t + 1 (+ 8), head g
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float p[4], w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            p[j] = ex2(x[nt][j] - ref[nt][j & 1]);
+            w[j] = FMT == A_FP8 ? ex2(y[nt][j] - refv[nt][j & 1]) : p[j];
+          }
+          l[nt][0] += p[0] + p[2];
+          l[nt][1] += p[1] + p[3];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            if constexpr (BF) {
+              const uint32_t hi2 = bf16x2(w[2 * r], w[2 * r + 1]);
+              pb[nt][r] = transpose8(hi2);
+              pl[nt][r] = transpose8(bf16x2(w[2 * r] - bf16_lo(hi2), w[2 * r + 1] - bf16_hi(hi2)));
+            } else {
+              pb[nt][r] = transpose8(f16x2(w[2 * r], w[2 * r + 1]));
+            }
+          }
+        }
+
+        // O^T: rows g and g + 8 are channels g (D / 8) + 2i and + 1
+        auto pv = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816<BF>(o[nt][i], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+            if constexpr (BF) mma16816<BF>(o[nt][i], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+          }
+        };
+#pragma unroll
+        for (int q = 0; q < D / 64; ++q) {
+          if constexpr (FMT == A_BF16) {
+            const uint4 v0 = vv4[(4 * q) * 32], v1 = vv4[(4 * q + 1) * 32], v2 = vv4[(4 * q + 2) * 32],
+                        v3 = vv4[(4 * q + 3) * 32];
+            const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w},
+                           w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              pv(4 * q + i, __byte_perm(w0[i], w1[i], 0x5410), __byte_perm(w0[i], w1[i], 0x7632),
+                 __byte_perm(w2[i], w3[i], 0x5410), __byte_perm(w2[i], w3[i], 0x7632));
+          } else if constexpr (FMT == A_FP8) {
+            const uint4 v0 = vv4[(2 * q) * 32], v1 = vv4[(2 * q + 1) * 32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t a = __byte_perm(i < 2 ? v0.x : v0.y, i < 2 ? v0.z : v0.w, (i & 1) ? 0x7362 : 0x5140);
+              const uint32_t c = __byte_perm(i < 2 ? v1.x : v1.y, i < 2 ? v1.z : v1.w, (i & 1) ? 0x7362 : 0x5140);
+              pv(4 * q + i, e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(c), e4m3x2_to_f16x2(c >> 16));
+            }
+          } else {
+            const uint4 v = vv4[q * 32];
+            const int blk = (g * (D / 64) + q) >> 1;
+            const uint16_t *vs = reinterpret_cast<const uint16_t *>(vsc + blk * 16);
+            const uint32_t s01 = e4m3x2_to_f16x2(vs[t]), s23 = e4m3x2_to_f16x2(vs[t + 4]);
+            const uint32_t m = 0x0f0f0f0fu;
+            const uint32_t e0 = (v.x & m) | ((v.y & m) << 4), e1 = ((v.x >> 4) & m) | (v.y & ~m);
+            const uint32_t e2 = (v.z & m) | ((v.w & m) << 4), e3 = ((v.z >> 4) & m) | (v.w & ~m);
+            pv(4 * q, hmul2(e2m1x2_to_f16x2<0>(e0), s01), hmul2(e2m1x2_to_f16x2<0>(e1), s01),
+               hmul2(e2m1x2_to_f16x2<0>(e2), s23), hmul2(e2m1x2_to_f16x2<0>(e3), s23));
+            pv(4 * q + 1, hmul2(e2m1x2_to_f16x2<1>(e0), s01), hmul2(e2m1x2_to_f16x2<1>(e1), s01),
+               hmul2(e2m1x2_to_f16x2<1>(e2), s23), hmul2(e2m1x2_to_f16x2<1>(e3), s23));
+            pv(4 * q + 2, hmul2(e2m1x2_to_f16x2<2>(e0), s01), hmul2(e2m1x2_to_f16x2<2>(e1), s01),
+               hmul2(e2m1x2_to_f16x2<2>(e2), s23), hmul2(e2m1x2_to_f16x2<2>(e3), s23));
+            pv(4 * q + 3, hmul2(e2m1x2_to_f16x2<3>(e0), s01), hmul2(e2m1x2_to_f16x2<3>(e1), s01),
+               hmul2(e2m1x2_to_f16x2<3>(e2), s23), hmul2(e2m1x2_to_f16x2<3>(e3), s23));
+          }
+        }
+      }
+
+      // the stage is read: fetch into it again
+      __syncwarp();
+      if (alive && to_issue > 0) issue(stage);
+      if (++stage == STAGES) {
+        stage = 0;
+        parity ^= 1u;
+      }
+      --left;
+      ++pos;
+
+      if (cw.u + 1 == cw.nu || left == 0) {  // the item, or this warp's part of it, is done
+        const long long start = pos - 1 - cw.u;
+        const bool begins = start >= c_begin + warp * c_units / W, ends = cw.u + 1 == cw.nu;
+        const int h = cw.it / a.hgroups, hg = cw.it % a.hgroups;
+        const int slot = begins ? 1 : 0;
+        float *rec = begins ? reinterpret_cast<float *>(ring) : rec0;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float s = l[nt][j];
+#pragma unroll
+            for (int k = 4; k < 32; k <<= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+            float f1 = s == 0.f ? 0.f : 1.f / s, f2 = 1.f;  // s is 0 where every page was missing
+            if constexpr (FMT == A_NVFP4) f1 *= a.kv.glob[1];
+            if constexpr (FMT == A_FP8) {
+              const float e = refv[nt][j] - ref[nt][j];  // in halves: the scales may span fp32
+              f1 *= ex2(0.5f * e);
+              f2 = ex2(0.5f * e);
+            }
+            const float lse2 = s == 0.f ? -INFINITY : ref[nt][j] + lg2(s);
+            const int hl = nt * 8 + 2 * t + j, hq = hg * GT + hl;
+            if (begins && ends) {
+              if (hq < a.group) {
+                const size_t row = (size_t)h * a.group + hq;
+                uint4 *dst = reinterpret_cast<uint4 *>(a.out + cw.b * a.os + row * D + g * (D / 8));
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    w[k] = bf16x2(o[nt][4 * i + k][j] * f1 * f2, o[nt][4 * i + k][2 + j] * f1 * f2);
+                  dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                if (a.lse && g == 0) a.lse[(size_t)cw.b * a.q_heads + row] = lse2 * 0.6931471805599453f;
+              }
+            } else {
+              float4 *dst = reinterpret_cast<float4 *>(rec + hl * D + g * (D / 8));
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i)
+                dst[i] = make_float4(o[nt][2 * i][j] * f1 * f2, o[nt][2 * i][2 + j] * f1 * f2,
+                                     o[nt][2 * i + 1][j] * f1 * f2, o[nt][2 * i + 1][2 + j] * f1 * f2);
+              if (g == 0) rec[GT * D + hl * 4] = lse2;
+            }
+          }
+        if (!(begins && ends) && lane == 0)
+          head->seg[2 * warp + slot] = AttnSeg{start, cw.b, cw.it, cw.nu, 1 | (begins ? 2 : 0) | (ends ? 4 : 0)};
+        fresh = true;
+      }
+      if (left > 0) cw.next(a, items);
+    }
+    if (!alive) {
+      // one more bounded wait for each stage, so that no copy lands after the CTA has gone
+      for (int s = 0; s < STAGES; ++s) {
+        mbar_wait(&full[stage], parity, WAIT_LIMIT_NS / 100);
+        if (++stage == STAGES) {
+          stage = 0;
+          parity ^= 1u;
+        }
+      }
+    }
+  }
+  __syncthreads();
+
+  // Join the parts that the CTA's warps left, in the order of the tokens: runs
+  // of segments of one item.
+  auto record = [&](int e) {
+    return e & 1 ? reinterpret_cast<const float *>(smem + ATTN_HEAD + (e >> 1) * (STAGES * UNIT))
+                 : reinterpret_cast<const float *>(smem + ATTN_HEAD + W * STAGES * UNIT) + (e >> 1) * (PART / 4);
+  };
+  auto finish = [&](int b, int it, int hl, int d, float4 v, float lse2) {  // 4 channels of one head
+    const int hq = (it % a.hgroups) * GT + hl;
+    if (hq >= a.group) return;
+    const size_t row = (size_t)(it / a.hgroups) * a.group + hq;
+    *reinterpret_cast<uint2 *>(a.out + b * a.os + row * D + d) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+    if (a.lse && d == 0) a.lse[(size_t)b * a.q_heads + row] = lse2 * 0.6931471805599453f;
+  };
+  int open = 0;  // records in the workspace: bit 0: of an item begun before, bit 1: of one that goes on
+  AttnSeg seg[2];
+  for (int e = 0; e < 2 * W;) {
+    const AttnSeg first = head->seg[e];
+    if (!first.flags) {
+      ++e;
+      continue;
+    }
+    int last = e, next = e + 1;
+    for (; next < 2 * W; ++next) {
+      if (!head->seg[next].flags) continue;
+      if (head->seg[next].start != first.start) break;
+      last = next;
+    }
+    const bool begins = first.flags & 2, ends = head->seg[last].flags & 4;
+    float *to = a.parts + ((size_t)blockIdx.x * 2 + (begins ? 1 : 0)) * (PART / 4);
+    for (int x = tid; x < GT * D / 4; x += W * 32) {
+      const int hl = x / (D / 4), d = (x % (D / 4)) * 4;
+      float m = -INFINITY, s = 0.f;
+      for (int i = e; i <= last; ++i)
+        if (head->seg[i].flags) m = fmaxf(m, record(i)[GT * D + hl * 4]);
+      const float r = m == -INFINITY ? 0.f : m;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = e; i <= last; ++i) {
+        if (!head->seg[i].flags) continue;
+        const float *rec = record(i);
+        const float w = ex2(rec[GT * D + hl * 4] - r);
+        const float4 p = *reinterpret_cast<const float4 *>(rec + hl * D + d);
+        s += w;
+        v.x += w * p.x; v.y += w * p.y; v.z += w * p.z; v.w += w * p.w;
+      }
+      const float inv = s == 0.f ? 0.f : 1.f / s, lse2 = s == 0.f ? -INFINITY : r + lg2(s);
+      v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
+      if (begins && ends) {
+        finish(first.b, first.it, hl, d, v, lse2);
+      } else {
+        __stcg(reinterpret_cast<float4 *>(to + hl * D + d), v);
+        if (d == 0) __stcg(to + GT * D + hl * 4, lse2);
+      }
+    }
+    if (!(begins && ends)) {
+      open |= begins ? 2 : 1;
+      seg[begins ? 1 : 0] = first;
+    }
+    e = next;
+  }
+  if (!open) return;
+
+  // Items that span CTAs: the last CTA to arrive joins their records.  The
+  // counter is that of the CTA in which the item begins.
+  __threadfence();
+  __syncthreads();
+  if (tid < 2) {
+    s_last[tid] = 0;
+    if (open >> tid & 1) {
+      const long long start = seg[tid].start;
+      const int c0 = attn_cta_of(start, total, ctas), c1 = attn_cta_of(start + seg[tid].nu - 1, total, ctas);
+      if (atomicAdd(&a.counters[c0], 1) == c1 - c0) {
+        a.counters[c0] = 0;
+        s_last[tid] = 1;
+      }
+      __threadfence();
+    }
+  }
+  __syncthreads();
+  for (int k = 0; k < 2; ++k) {
+    if (!s_last[k]) continue;
+    const long long start = seg[k].start;
+    const int c0 = attn_cta_of(start, total, ctas), c1 = attn_cta_of(start + seg[k].nu - 1, total, ctas);
+    for (int x = tid; x < GT * D / 4; x += W * 32) {
+      const int hl = x / (D / 4), d = (x % (D / 4)) * 4;
+      float m = -INFINITY, s = 0.f;
+      auto from = [&](int c) { return a.parts + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * (PART / 4); };
+      for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(from(c) + GT * D + hl * 4));
+      const float r = m == -INFINITY ? 0.f : m;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = c0; c <= c1; ++c) {
+        const float *rec = from(c);
+        const float w = ex2(__ldcg(rec + GT * D + hl * 4) - r);
+        const float4 p = __ldcg(reinterpret_cast<const float4 *>(rec + hl * D + d));
+        s += w;
+        v.x += w * p.x; v.y += w * p.y; v.z += w * p.z; v.w += w * p.w;
+      }
+      const float inv = s == 0.f ? 0.f : 1.f / s, lse2 = s == 0.f ? -INFINITY : r + lg2(s);
+      v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
+      finish(seg[k].b, seg[k].it, hl, d, v, lse2);
+    }
+  }
+}
+
+// Eight-head tiles per item: a second one from nine query heads per kv head
+// on, so that the cache is read once for up to 16; larger groups read it once
+// per 16 heads, mostly from L2.
+static int attn_tiles(int group) { return group <= 8 ? 1 : 2; }
+
+size_t attn_workspace_bytes(int D, int group, int sms) {
+  return align_up((size_t)sms * sizeof(int), 256) + (size_t)sms * 2 * (8 * attn_tiles(group)) * (D + 4) * sizeof(float);
+}
+
+template <int FMT, int D, int NT>
+static hq_status attn_start(const AttnArgs &a, int sms, cudaStream_t st) {
+  using S = AttnShape<FMT, D, NT>;
+  static unsigned configured = 0;  // devices whose shared-memory limit is raised
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return HQ_ERR_CUDA;
+  if (dev >= 32 || !(configured & (1u << dev))) {
+    if (cudaFuncSetAttribute(attn_kernel<FMT, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) != cudaSuccess)
+      return HQ_ERR_CUDA;
+    if (dev < 32) configured |= 1u << dev;
+  }
+  attn_kernel<FMT, D, NT><<<sms, S::W * 32, S::SMEM, st>>>(a);
+  return check_launch();
+}
+
+hq_status launch_attn(int fmt, int D, AttnArgs a, int sms, void *workspace, cudaStream_t st) {
+  const int nt = attn_tiles(a.group);
+  a.hgroups = (a.group + 8 * nt - 1) / (8 * nt);
+  a.counters = (int *)workspace;
+  a.parts = (float *)((uint8_t *)workspace + align_up((size_t)sms * sizeof(int), 256));
   return kv_dispatch(fmt, D, [&](auto F, auto DD) {
-    attn_kernel<F, DD><<<a.B * a.q_heads, 128, 0, st>>>(a);
-    return check_launch();
+    return nt == 1 ? attn_start<F, DD, 1>(a, sms, st) : attn_start<F, DD, 2>(a, sms, st);
   });
 }
 
