@@ -174,9 +174,24 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_torch = None
+
+
+def _cuda():
+    """torch, imported when a call first needs it."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _stream(stream):
     if stream is None:
-        import torch
+        torch = _cuda()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 0.1 us; the Stream object takes 3
+        if raw is not None and torch.cuda.is_initialized():
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -337,14 +352,15 @@ def hq_moe_gemm_gated(mode, desc, T, topk, E, I, K, packed_w, a, a_scales, a_glo
 def _on_device(fn, *tensors):
     """Device pointers of tensors (None and integer addresses pass): each has
     to be on the current CUDA device, whose stream the call runs on."""
-    import torch
-    dev = torch.cuda.current_device() if any(hasattr(t, "data_ptr") and t.is_cuda for t in tensors) else -2
-    out = []
+    dev, out = None, []
     for t in tensors:
-        if t is None or isinstance(t, int):
+        if t is None or type(t) is int:
             out.append(t)
             continue
-        if t.get_device() != dev:
+        d = t.get_device()
+        if dev is None and d >= 0:
+            dev = _cuda().cuda.current_device()
+        if d < 0 or d != dev:
             raise HQError(fn, 1)
         out.append(t.data_ptr())
     return out

@@ -4,6 +4,7 @@
 // hq_device_error, whose job is to synchronise).
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstring>
 
 #include "hq_internal.cuh"
@@ -47,13 +48,23 @@ hq_status check_launch() {
   return e == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
 }
 
+// Whether the current device is sm_100; asked of the runtime once per device
+// (the two attribute queries cost a microsecond, as much as the rest of a call).
 bool device_is_sm100() {
+  static std::atomic<signed char> known[32];  // 0: not asked, 1: yes, -1: no
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const bool keep = dev >= 0 && dev < 32;
+  if (keep) {
+    const signed char k = known[dev].load(std::memory_order_relaxed);
+    if (k) return k > 0;
+  }
   int major = 0, minor = 0;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return false;
   if (cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) return false;
-  return major == 10 && minor == 0;
+  const bool yes = major == 10 && minor == 0;
+  if (keep) known[dev].store(yes ? 1 : -1, std::memory_order_relaxed);
+  return yes;
 }
 
 static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -833,6 +844,9 @@ hq_status hq_kv_read(const hq_kv_desc *kv, int T, const int64_t *slots, const fl
   return launch_kv_read(fmt, kv->head_dim, a, w, (cudaStream_t)stream);
 }
 
+// One persistent CTA per SM.
+static int attn_ctas() { return device_sm_count() < ATTN_MAX_CTAS ? device_sm_count() : ATTN_MAX_CTAS; }
+
 static bool valid_q_heads(const hq_kv_desc *kv, int B, int q_heads) {
   return B >= 0 && B <= (1 << 20) && q_heads >= kv->heads && q_heads <= 65536 && (q_heads % kv->heads) == 0;
 }
@@ -840,7 +854,7 @@ static bool valid_q_heads(const hq_kv_desc *kv, int B, int q_heads) {
 size_t hq_paged_attn_workspace_bytes(const hq_kv_desc *kv, int B, int q_heads) {
   int fmt;
   if (check_kv(kv, &fmt) != HQ_OK || !valid_q_heads(kv, B, q_heads)) return 0;
-  return attn_workspace_bytes(kv->head_dim, q_heads / kv->heads, device_sm_count());
+  return attn_workspace_bytes(fmt, kv->head_dim, q_heads / kv->heads, attn_ctas());
 }
 
 hq_status hq_paged_attn(const hq_kv_desc *kv, int B, int q_heads, const void *q_bf16, int64_t q_stride,
@@ -860,8 +874,8 @@ hq_status hq_paged_attn(const hq_kv_desc *kv, int B, int q_heads, const void *q_
   const hq_status ps = check_pages(kv, num_pages, pages, global_scale);
   if (ps != HQ_OK) return ps;
   const int group = q_heads / kv->heads;
-  const int sms = device_sm_count();
-  if (!workspace || !aligned16(workspace) || ws_bytes < attn_workspace_bytes(kv->head_dim, group, sms))
+  const int sms = attn_ctas();
+  if (!workspace || !aligned16(workspace) || ws_bytes < attn_workspace_bytes(fmt, kv->head_dim, group, sms))
     return HQ_ERR_WORKSPACE;
   if (!device_is_sm100()) return HQ_ERR_ARCH;
   AttnArgs a{};

@@ -137,36 +137,56 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 // ---- shape of a kernel ---------------------------------------------------------
-// NT = 8-head tiles per item.  W warps, each with a ring of STAGES units.  A
-// partial record is GT x D normalised outputs and GT log2 sums; a warp keeps
-// at most two, one of them in its drained ring.
-constexpr int ATTN_SMEM = 227 * 1024 - 512;  // what a CTA may have, less the static part
-constexpr int ATTN_HEAD = 1280;              // barriers and bookkeeping
+// NT = 8-head tiles per item.  W consumer warps, each with a ring of STAGES
+// units, and one producer warp.  A partial record is GT x D normalised outputs
+// and GT log2 sums; a warp leaves at most two: one in its drained ring, the
+// other, written while the ring is in use, beside the rings or, where records
+// are large, in the workspace (so in L2).
+constexpr int ATTN_SMEM = 227 * 1024 - 1024;  // what a CTA may have, less the static part
+constexpr int ATTN_HEAD = 8192;               // barriers and bookkeeping
+constexpr int ATTN_MAX_CTAS = 256;
 template <int FMT, int D, int NT>
 struct AttnShape {
   static constexpr int GT = 8 * NT;
   static constexpr int UNIT = kv_unit_bytes(FMT, D);
   static constexpr int PART = GT * (D + 4) * 4;  // bytes; the sums padded to 16 per head
-  static constexpr int fit(int w) { return ((ATTN_SMEM - ATTN_HEAD) / w - PART) / UNIT; }
-  static constexpr int W = fit(8) >= 3 ? 8 : 4;
+  static constexpr bool FAR = GT * D >= 2048;    // first records in the workspace
+  static constexpr int fit(int w) { return ((ATTN_SMEM - ATTN_HEAD) / w - (FAR ? 0 : PART)) / UNIT; }
+  // The producer makes W + 1 warps a multiple of four, one per scheduler: 16
+  // warps may have 128 registers a lane, 12 168 and 8 or 4 255.  Of the counts that the registers
+  // allow (6 per output tile and 16 channels, and some 70 more), the largest
+  // that keeps 120 KB on its way.
+  static constexpr int REGS = NT * (D / 16) * 6;
+  static constexpr bool deep(int w) { return fit(w) >= 2 && w * fit(w) * UNIT >= 120 * 1024; }
+  static constexpr int W = REGS <= 48 && deep(15) ? 15 : REGS <= 96 && deep(11) ? 11 : deep(7) ? 7 : 3;
   static constexpr int STAGES = fit(W) < 12 ? fit(W) : 12;
-  static constexpr int SMEM = ATTN_HEAD + W * (PART + STAGES * UNIT);
-  static_assert(STAGES >= 2 && STAGES * UNIT >= PART, "ring too small");
+  static constexpr int SMEM = ATTN_HEAD + W * ((FAR ? 0 : PART) + STAGES * UNIT);
+  static constexpr size_t workspace(int sms) {  // after the counters
+    return (size_t)sms * PART * (2 + (FAR ? W : 0));
+  }
+  static_assert(STAGES >= 2 && STAGES * UNIT >= PART && W * STAGES * UNIT >= GT * ATTN_MAX_CTAS * 4, "ring too small");
 };
+constexpr int ATTN_RINGS = 15 * 12;  // most (warp, stage) pairs
 
+struct AttnUnit {        // what the producer says of a unit
+  int b, it, u, nu;      // sequence, head group, the unit's place in its item and the item's units
+};
 struct AttnSeg {         // a part of an item that a warp leaves behind
   long long start;       // the item's first unit in the line
-  int b, it, nu;         // sequence, head group, units of the item
+  int b, it, nu;
   int flags;             // 1: present, 2: holds the item's first unit, 4: its last
 };
 
 struct AttnHead {
-  uint64_t full[96];     // [W][STAGES]
-  AttnSeg seg[16];       // [W][2]
+  uint64_t full[ATTN_RINGS], empty[ATTN_RINGS];
+  AttnUnit unit[ATTN_RINGS];
+  int meta[ATTN_RINGS];  // valid tokens [lo, hi) in bits 0..4 and 5..9, and flags:
+  AttnSeg seg[30];       // [W][2]
 };
+enum { ATTN_LAST = 1024, ATTN_BAD = 2048 };  // the item's last unit; a page that does not exist
 struct AttnStart {
-  long long off[8];
-  int b[8];
+  long long off[15];
+  int b[15];
 };
 
 // A walk along the line of units.
@@ -177,7 +197,7 @@ struct AttnWalk {
     u0 = first / 16;
     nu = len ? (int)(((long long)len + 15) / 16) - u0 : 0;
   }
-  // to the next unit; there is one
+  // to the next unit; there is one.  True if it is another item's.
   __device__ __forceinline__ bool next(const AttnArgs &a, int items) {
     if (++u < nu) return false;
     u = 0;
@@ -191,37 +211,60 @@ struct AttnWalk {
   }
 };
 
+// n / d, in 32 bits where both fit (a 64-bit division is some hundred cycles)
+__device__ __forceinline__ long long attn_div(long long n, long long d) {
+  return (n | d) >> 32 ? n / d : (long long)((uint32_t)n / (uint32_t)d);
+}
+// CTA c of `ctas` has the units from floor(c total / ctas) on; the CTA of unit u
 __device__ __forceinline__ int attn_cta_of(long long u, long long total, int ctas) {
-  return (int)(((u + 1) * ctas - 1) / total);
+  return (int)attn_div((u + 1) * ctas - 1, total);
+}
+
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {  // does not suspend the warp
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32, 1) attn_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + 32, 1) attn_kernel(AttnArgs a) {
   using S = AttnShape<FMT, D, NT>;
   constexpr int W = S::W, STAGES = S::STAGES, UNIT = S::UNIT, GT = S::GT, PART = S::PART;
   constexpr int CB = kv_code_bytes(FMT, D), SB = kv_scale_bytes(FMT, D);
+  constexpr int THREADS = W * 32 + 32;
   constexpr bool BF = FMT == A_BF16;
   constexpr float LIM = BF ? 8.f : 15.f, SHIFT = BF ? 0.f : 10.f;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long s_scan[W + 1];
   __shared__ AttnStart s_start;
   __shared__ int s_last[2];
+  __shared__ float s_lse[GT];
+  __shared__ volatile int s_stop;
   AttnHead *head = reinterpret_cast<AttnHead *>(smem);
-  static_assert(sizeof(AttnHead) <= ATTN_HEAD && W * STAGES <= 96, "bookkeeping");
+  static_assert(sizeof(AttnHead) <= ATTN_HEAD && W * STAGES <= ATTN_RINGS, "bookkeeping");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  uint8_t *ring = smem + ATTN_HEAD + warp * (STAGES * UNIT);
-  float *rec0 = reinterpret_cast<float *>(smem + ATTN_HEAD + W * STAGES * UNIT) + warp * (PART / 4);
-  uint64_t *full = head->full + warp * STAGES;
   const int items = a.kv.H * a.hgroups;
+  auto near_record = [&](int w) {  // a warp's part of an item begun before
+    return S::FAR ? a.parts + ((size_t)gridDim.x * 2 + (size_t)blockIdx.x * W + w) * (PART / 4)
+                  : reinterpret_cast<float *>(smem + ATTN_HEAD + W * STAGES * UNIT) + w * (PART / 4);
+  };
 
-  if (lane == 0) {
-    for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1);
-    head->seg[2 * warp].flags = head->seg[2 * warp + 1].flags = 0;
+  if (tid < W * STAGES) {
+    mbar_init(&head->full[tid], 1);
+    mbar_init(&head->empty[tid], 1);
     fence_barrier_init();
   }
+  if (tid < 2 * W) head->seg[tid].flags = 0;
+  if (tid == 0) s_stop = 0;
 
   // empty sequences: zeros, written by whoever comes by
-  for (int b0 = (blockIdx.x * W + warp) * 32; b0 < a.B; b0 += gridDim.x * W * 32) {
+  for (int b0 = (blockIdx.x * (W + 1) + warp) * 32; b0 < a.B; b0 += gridDim.x * THREADS) {
     unsigned empty = __ballot_sync(0xffffffffu, b0 + lane < a.B && attn_units(a, min(b0 + lane, a.B - 1)) == 0);
     while (empty) {
       const int b = b0 + __ffs(empty) - 1;
@@ -234,7 +277,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32, 1) attn_kernel(
   }
 
   // the line's length, and where each of this CTA's warps starts
-  const int per = (a.B + W * 32 - 1) / (W * 32);
+  const int per = (a.B + THREADS - 1) / THREADS;
   const int bs = min(tid * per, a.B), be = min(bs + per, a.B);
   long long mine = 0;
   for (int b = bs; b < be; ++b) mine += attn_units(a, b);
@@ -248,7 +291,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32, 1) attn_kernel(
   __syncthreads();
   long long before = incl - mine, sum = 0;
 #pragma unroll
-  for (int w = 0; w < W; ++w) {
+  for (int w = 0; w <= W; ++w) {
     if (w < warp) before += s_scan[w];
     sum += s_scan[w];
   }
@@ -256,7 +299,8 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32, 1) attn_kernel(
   const long long want = (total + W - 1) / W;  // a unit per warp at least
   const int ctas = (int)(want < gridDim.x ? want : gridDim.x);
   if ((int)blockIdx.x >= ctas) return;
-  const long long c_begin = blockIdx.x * total / ctas, c_units = (blockIdx.x + 1) * total / ctas - c_begin;
+  const long long c_begin = attn_div(blockIdx.x * total, ctas);
+  const long long c_units = attn_div((blockIdx.x + 1) * total, ctas) - c_begin;
   if (mine) {
     for (int w = 0; w < W; ++w) {
       const long long at = c_begin + w * c_units / W;
@@ -275,71 +319,112 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32, 1) attn_kernel(
   }
   __syncthreads();
 
-  long long pos = c_begin + warp * c_units / W;  // the next unit to compute, along the line
-  int left = (int)(c_begin + (warp + 1) * c_units / W - pos);
-  if (left > 0) {
-    AttnWalk cw;  // what is computed
-    cw.b = s_start.b[warp];
-    cw.open(a);
-    cw.it = (int)(s_start.off[warp] / cw.nu);
-    cw.u = (int)(s_start.off[warp] % cw.nu);
-    AttnWalk pw = cw;  // what is fetched
+  if (warp == W) {
+    // The producer: lane w walks consumer warp w's part of the line.
+    AttnWalk pw{};
+    int to_issue = 0, issued = 0, stage = 0, pidx = 0, psub = 0, pg = 0;
+    uint32_t parity = 1;
     const int upp = a.kv.page_units;
-    int pidx = (pw.u0 + pw.u) / upp, psub = (pw.u0 + pw.u) % upp;
-    int cache_b = -1, cache_at = 0, cached = 0;
-    int to_issue = left;
-    unsigned bad = 0;  // stages whose page does not exist
-
-    auto issue = [&](int stage) {
-      if (pw.b != cache_b || pidx < cache_at || pidx >= cache_at + 32) {
-        cache_b = pw.b;
-        cache_at = pidx;
-        // only pages the sequence reaches are read
-        cached = pidx + lane < (pw.len + a.kv.page - 1) / a.kv.page
-                     ? a.page_table[(size_t)pw.b * a.max_pages + pidx + lane] : 0;
+    auto locate = [&]() {
+      pidx = (pw.u0 + pw.u) / upp;
+      psub = (pw.u0 + pw.u) - pidx * upp;
+      pg = a.page_table[(size_t)pw.b * a.max_pages + pidx];
+    };
+    if (lane < W) {
+      to_issue = (int)((lane + 1) * c_units / W - lane * c_units / W);
+      if (to_issue > 0) {
+        pw.b = s_start.b[lane];
+        pw.open(a);
+        pw.it = (int)attn_div(s_start.off[lane], pw.nu);
+        pw.u = (int)(s_start.off[lane] - (long long)pw.it * pw.nu);
+        locate();
       }
-      const int pg = __shfl_sync(0xffffffffu, cached, pidx - cache_at);
-      const bool ok = pg >= 0 && pg < a.num_pages;
-      bad = ok ? bad & ~(1u << stage) : bad | (1u << stage);
-      if (lane == 0) {
+    }
+    unsigned long long idle = 0;
+    while (__any_sync(0xffffffffu, to_issue > 0)) {
+      const int slot = lane * STAGES + stage;
+      const bool ready = to_issue > 0 && (issued < STAGES || mbar_test(&head->empty[slot], parity));
+      if (ready) {
+        const int tok0 = (pw.u0 + pw.u) * 16;
+        const bool ok = pg >= 0 && pg < a.num_pages;
+        head->unit[slot] = AttnUnit{pw.b, pw.it, pw.u, pw.nu};
+        head->meta[slot] = max(pw.first - tok0, 0) | min(pw.len - tok0, 16) << 5 | (pw.u + 1 == pw.nu ? ATTN_LAST : 0) |
+                           (ok ? 0 : ATTN_BAD);
         if (ok) {
           const uint8_t *src = a.kv.pages + (size_t)pg * a.kv.page_bytes +
                                ((size_t)(pw.it / a.hgroups) * upp + psub) * UNIT;
-          mbar_arrive_expect_tx(&full[stage], UNIT);
-          bulk_g2s(ring + stage * UNIT, src, UNIT, &full[stage]);
+          mbar_arrive_expect_tx(&head->full[slot], UNIT);
+          bulk_g2s(smem + ATTN_HEAD + slot * UNIT, src, UNIT, &head->full[slot]);
         } else {
           set_device_error(HQ_ERR_DEVICE_INDEX);
-          mbar_arrive(&full[stage]);
+          mbar_arrive(&head->full[slot]);
+        }
+        ++issued;
+        if (++stage == STAGES) {
+          stage = 0;
+          parity ^= 1u;
+        }
+        if (--to_issue > 0) {
+          if (pw.next(a, items)) {
+            locate();
+          } else if (++psub == upp) {
+            psub = 0;
+            pg = a.page_table[(size_t)pw.b * a.max_pages + ++pidx];
+          }
         }
       }
-      if (--to_issue > 0) {
-        if (pw.next(a, items)) {
-          pidx = (pw.u0 + pw.u) / upp;
-          psub = (pw.u0 + pw.u) % upp;
-        } else if (++psub == upp) {
-          psub = 0;
-          ++pidx;
-        }
+      if (__any_sync(0xffffffffu, ready)) {
+        idle = 0;
+      } else {
+        __nanosleep(32);
+        const unsigned long long now = __shfl_sync(0xffffffffu, global_timer_ns(), 0);
+        if (idle == 0) idle = now;
+        const bool late = now - idle > WAIT_LIMIT_NS;
+        if (late) set_device_error(HQ_ERR_TIMEOUT);
+        if (__any_sync(0xffffffffu, late || s_stop)) break;
       }
-    };
-    for (int s = 0; s < STAGES && to_issue > 0; ++s) issue(s);
-
+    }
+  }
+  const long long w_begin = warp < W ? warp * c_units / W : 0;
+  int left = warp < W ? (int)((warp + 1) * c_units / W - w_begin) : 0;
+  if (left > 0) {
+    long long pos = c_begin + w_begin;  // the next unit, along the line
+    uint8_t *ring = smem + ATTN_HEAD + warp * (STAGES * UNIT);
+    float *rec0 = near_record(warp);
+    AttnUnit cu{};          // the item at hand
+    long long item_start = 0;
     uint32_t qf[NT][D / 16][2];  // B fragments of q: k = this lane's channels, n = head g
     float qc[NT][2];             // score multiplier of heads 2t, 2t + 1
     float o[NT][D / 16][4], l[NT][2], ref[NT][2], refv[NT][2];
-    bool fresh = true, alive = true;
+    bool fresh = true;
     int stage = 0;
     uint32_t parity = 0;
 
     while (left > 0) {
+      const int slot = warp * STAGES + stage;
+      if (!__all_sync(0xffffffffu, mbar_wait(&head->full[slot], parity))) {
+        // gave up (recorded): stop the copies, and give those in flight time to land before the CTA goes
+        s_stop = 1;
+        for (int k = 0; k < STAGES; ++k) {
+          mbar_wait(&head->full[warp * STAGES + stage], parity, WAIT_LIMIT_NS / 100);
+          if (++stage == STAGES) {
+            stage = 0;
+            parity ^= 1u;
+          }
+        }
+        break;
+      }
+      const int meta = head->meta[slot];
       if (fresh) {
         fresh = false;
-        const int h = cw.it / a.hgroups, hg = cw.it % a.hgroups;
+        cu = head->unit[slot];
+        item_start = pos - cu.u;
+        const int h = cu.it / a.hgroups, hg = cu.it % a.hgroups;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const int hq = hg * GT + nt * 8 + g;
           const bool on = hq < a.group;
-          const uint16_t *src = a.q + cw.b * a.qs + (size_t)(h * a.group + (on ? hq : 0)) * D + 8 * t;
+          const uint16_t *src = a.q + cu.b * a.qs + (size_t)(h * a.group + (on ? hq : 0)) * D + 8 * t;
           uint4 v[D / 32];
           float amax = 0.f;
 #pragma unroll
@@ -392,15 +477,12 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32, 1) attn_kernel(
         }
       }
 
-      // a wait that gave up (recorded) ends the warp's copies; those in flight are waited for once, below
-      if (alive) alive = __all_sync(0xffffffffu, mbar_wait(&full[stage], parity));
-      if (alive && !(bad >> stage & 1u)) {
+      if (!(meta & ATTN_BAD)) {
         uint8_t *unit = ring + stage * UNIT;
         const uint4 *kv4 = reinterpret_cast<const uint4 *>(unit) + lane;
         const uint4 *vv4 = reinterpret_cast<const uint4 *>(unit + CB) + lane;
         const uint8_t *ksc = unit + 2 * CB, *vsc = ksc + SB;
-        const int tok0 = (cw.u0 + cw.u) * 16;
-        const int lo = cw.first - tok0, hi = cw.len - tok0;  // valid tokens: [lo, hi) of 0..15
+        const int lo = meta & 31, hi = meta >> 5 & 31;  // valid tokens
         const bool edge = lo > 0 || hi < 16;
         if (edge) {
           // what lies past the sequence may be NaN, and 0 * NaN is: zero the values this lane reads
@@ -594,9 +676,8 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32, 1) attn_kernel(
         }
       }
 
-      // the stage is read: fetch into it again
       __syncwarp();
-      if (alive && to_issue > 0) issue(stage);
+      if (lane == 0) mbar_arrive(&head->empty[slot]);
       if (++stage == STAGES) {
         stage = 0;
         parity ^= 1u;
@@ -604,11 +685,9 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32, 1) attn_kernel(
       --left;
       ++pos;
 
-      if (cw.u + 1 == cw.nu || left == 0) {  // the item, or this warp's part of it, is done
-        const long long start = pos - 1 - cw.u;
-        const bool begins = start >= c_begin + warp * c_units / W, ends = cw.u + 1 == cw.nu;
-        const int h = cw.it / a.hgroups, hg = cw.it % a.hgroups;
-        const int slot = begins ? 1 : 0;
+      if ((meta & ATTN_LAST) || left == 0) {  // the item, or this warp's part of it, is done
+        const bool begins = item_start >= c_begin + w_begin, ends = meta & ATTN_LAST;
+        const int h = cu.it / a.hgroups, hg = cu.it % a.hgroups;
         float *rec = begins ? reinterpret_cast<float *>(ring) : rec0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -629,7 +708,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32, 1) attn_kernel(
             if (begins && ends) {
               if (hq < a.group) {
                 const size_t row = (size_t)h * a.group + hq;
-                uint4 *dst = reinterpret_cast<uint4 *>(a.out + cw.b * a.os + row * D + g * (D / 8));
+                uint4 *dst = reinterpret_cast<uint4 *>(a.out + cu.b * a.os + row * D + g * (D / 8));
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i) {
                   uint32_t w[4];
@@ -638,7 +717,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32, 1) attn_kernel(
                     w[k] = bf16x2(o[nt][4 * i + k][j] * f1 * f2, o[nt][4 * i + k][2 + j] * f1 * f2);
                   dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                if (a.lse && g == 0) a.lse[(size_t)cw.b * a.q_heads + row] = lse2 * 0.6931471805599453f;
+                if (a.lse && g == 0) a.lse[(size_t)cu.b * a.q_heads + row] = lse2 * 0.6931471805599453f;
               }
             } else {
               float4 *dst = reinterpret_cast<float4 *>(rec + hl * D + g * (D / 8));
@@ -650,19 +729,9 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32, 1) attn_kernel(
             }
           }
         if (!(begins && ends) && lane == 0)
-          head->seg[2 * warp + slot] = AttnSeg{start, cw.b, cw.it, cw.nu, 1 | (begins ? 2 : 0) | (ends ? 4 : 0)};
+          head->seg[2 * warp + (begins ? 1 : 0)] =
+              AttnSeg{item_start, cu.b, cu.it, cu.nu, 1 | (begins ? 2 : 0) | (ends ? 4 : 0)};
         fresh = true;
-      }
-      if (left > 0) cw.next(a, items);
-    }
-    if (!alive) {
-      // one more bounded wait for each stage, so that no copy lands after the CTA has gone
-      for (int s = 0; s < STAGES; ++s) {
-        mbar_wait(&full[stage], parity, WAIT_LIMIT_NS / 100);
-        if (++stage == STAGES) {
-          stage = 0;
-          parity ^= 1u;
-        }
       }
     }
   }
@@ -672,7 +741,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32, 1) attn_kernel(
   // of segments of one item.
   auto record = [&](int e) {
     return e & 1 ? reinterpret_cast<const float *>(smem + ATTN_HEAD + (e >> 1) * (STAGES * UNIT))
-                 : reinterpret_cast<const float *>(smem + ATTN_HEAD + W * STAGES * UNIT) + (e >> 1) * (PART / 4);
+                 : near_record(e >> 1);
   };
   auto finish = [&](int b, int it, int hl, int d, float4 v, float lse2) {  // 4 channels of one head
     const int hq = (it % a.hgroups) * GT + hl;
@@ -697,7 +766,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32, 1) attn_kernel(
     }
     const bool begins = first.flags & 2, ends = head->seg[last].flags & 4;
     float *to = a.parts + ((size_t)blockIdx.x * 2 + (begins ? 1 : 0)) * (PART / 4);
-    for (int x = tid; x < GT * D / 4; x += W * 32) {
+    for (int x = tid; x < GT * D / 4; x += THREADS) {
       const int hl = x / (D / 4), d = (x % (D / 4)) * 4;
       float m = -INFINITY, s = 0.f;
       for (int i = e; i <= last; ++i)
@@ -748,26 +817,40 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32, 1) attn_kernel(
   __syncthreads();
   for (int k = 0; k < 2; ++k) {
     if (!s_last[k]) continue;
-    const long long start = seg[k].start;
-    const int c0 = attn_cta_of(start, total, ctas), c1 = attn_cta_of(start + seg[k].nu - 1, total, ctas);
-    for (int x = tid; x < GT * D / 4; x += W * 32) {
-      const int hl = x / (D / 4), d = (x % (D / 4)) * 4;
+    const int c0 = attn_cta_of(seg[k].start, total, ctas);
+    const int n = attn_cta_of(seg[k].start + seg[k].nu - 1, total, ctas) - c0 + 1;
+    // the records: c0's is of an item begun there, the others' of one begun before
+    const float *recs = a.parts + (size_t)c0 * 2 * (PART / 4);
+    auto rec = [&](int c) { return recs + ((size_t)c * 2 + (c == 0 ? 1 : 0)) * (PART / 4); };
+    float *weight = reinterpret_cast<float *>(smem + ATTN_HEAD);  // [GT][n], where the rings were
+    for (int i = tid; i < GT * n; i += THREADS) weight[i] = __ldcg(rec(i % n) + GT * D + i / n * 4);
+    __syncthreads();
+    for (int hl = warp; hl < GT; hl += W + 1) {
       float m = -INFINITY, s = 0.f;
-      auto from = [&](int c) { return a.parts + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * (PART / 4); };
-      for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(from(c) + GT * D + hl * 4));
+      for (int c = lane; c < n; c += 32) m = fmaxf(m, weight[hl * n + c]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       const float r = m == -INFINITY ? 0.f : m;
+      for (int c = lane; c < n; c += 32) s += ex2(weight[hl * n + c] - r);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      const float inv = s == 0.f ? 0.f : 1.f / s;
+      for (int c = lane; c < n; c += 32) weight[hl * n + c] = ex2(weight[hl * n + c] - r) * inv;
+      if (lane == 0) s_lse[hl] = s == 0.f ? -INFINITY : r + lg2(s);
+    }
+    __syncthreads();
+    for (int x = tid; x < GT * D / 4; x += THREADS) {
+      const int hl = x / (D / 4), d = (x % (D / 4)) * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int c = c0; c <= c1; ++c) {
-        const float *rec = from(c);
-        const float w = ex2(__ldcg(rec + GT * D + hl * 4) - r);
-        const float4 p = __ldcg(reinterpret_cast<const float4 *>(rec + hl * D + d));
-        s += w;
+#pragma unroll 8
+      for (int c = 0; c < n; ++c) {
+        const float w = weight[hl * n + c];
+        const float4 p = __ldcg(reinterpret_cast<const float4 *>(rec(c) + hl * D + d));
         v.x += w * p.x; v.y += w * p.y; v.z += w * p.z; v.w += w * p.w;
       }
-      const float inv = s == 0.f ? 0.f : 1.f / s, lse2 = s == 0.f ? -INFINITY : r + lg2(s);
-      v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
-      finish(seg[k].b, seg[k].it, hl, d, v, lse2);
+      finish(seg[k].b, seg[k].it, hl, d, v, s_lse[hl]);
     }
+    __syncthreads();
   }
 }
 
@@ -776,8 +859,13 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32, 1) attn_kernel(
 // per 16 heads, mostly from L2.
 static int attn_tiles(int group) { return group <= 8 ? 1 : 2; }
 
-size_t attn_workspace_bytes(int D, int group, int sms) {
-  return align_up((size_t)sms * sizeof(int), 256) + (size_t)sms * 2 * (8 * attn_tiles(group)) * (D + 4) * sizeof(float);
+size_t attn_workspace_bytes(int fmt, int D, int group, int sms) {
+  size_t n = 0;
+  kv_dispatch(fmt, D, [&](auto F, auto DD) {
+    n = attn_tiles(group) == 1 ? AttnShape<F, DD, 1>::workspace(sms) : AttnShape<F, DD, 2>::workspace(sms);
+    return HQ_OK;
+  });
+  return align_up((size_t)sms * sizeof(int), 256) + n;
 }
 
 template <int FMT, int D, int NT>
@@ -791,7 +879,7 @@ static hq_status attn_start(const AttnArgs &a, int sms, cudaStream_t st) {
       return HQ_ERR_CUDA;
     if (dev < 32) configured |= 1u << dev;
   }
-  attn_kernel<FMT, D, NT><<<sms, S::W * 32, S::SMEM, st>>>(a);
+  attn_kernel<FMT, D, NT><<<sms, S::W * 32 + 32, S::SMEM, st>>>(a);
   return check_launch();
 }
 
