@@ -143,7 +143,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 // other, written while the ring is in use, beside the rings or, where records
 // are large, in the workspace (so in L2).
 constexpr int ATTN_SMEM = 227 * 1024 - 1024;  // what a CTA may have, less the static part
-constexpr int ATTN_HEAD = 8192;               // barriers and bookkeeping
+constexpr int ATTN_HEAD = 11520;              // barriers and bookkeeping
 constexpr int ATTN_MAX_CTAS = 256;
 template <int FMT, int D, int NT>
 struct AttnShape {
@@ -182,13 +182,9 @@ struct AttnHead {
   AttnUnit unit[ATTN_RINGS];
   int meta[ATTN_RINGS];  // valid tokens [lo, hi) in bits 0..4 and 5..9, and flags:
   AttnSeg seg[30];       // [W][2]
+  long long before[512]; // units of the sequences before a thread's share
 };
 enum { ATTN_LAST = 1024, ATTN_BAD = 2048 };  // the item's last unit; a page that does not exist
-struct AttnStart {
-  long long off[15];
-  int b[15];
-};
-
 // A walk along the line of units.
 struct AttnWalk {
   int b, it, u, nu, u0, len, first;
@@ -242,8 +238,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + 32, 1) attn_ke
   constexpr float LIM = BF ? 8.f : 15.f, SHIFT = BF ? 0.f : 10.f;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long s_scan[W + 1];
-  __shared__ AttnStart s_start;
-  __shared__ int s_last[2];
+  __shared__ int s_last[2], s_from[4];
   __shared__ float s_lse[GT];
   __shared__ volatile int s_stop;
   AttnHead *head = reinterpret_cast<AttnHead *>(smem);
@@ -263,24 +258,24 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + 32, 1) attn_ke
   if (tid < 2 * W) head->seg[tid].flags = 0;
   if (tid == 0) s_stop = 0;
 
-  // empty sequences: zeros, written by whoever comes by
-  for (int b0 = (blockIdx.x * (W + 1) + warp) * 32; b0 < a.B; b0 += gridDim.x * THREADS) {
-    unsigned empty = __ballot_sync(0xffffffffu, b0 + lane < a.B && attn_units(a, min(b0 + lane, a.B - 1)) == 0);
+  // The line's length: each thread counts the units of its share of the
+  // sequences.  Empty sequences get their zeros from one of the CTAs.
+  const int per = (a.B + THREADS - 1) / THREADS;
+  long long mine = 0;
+  for (int k = 0; k < per; ++k) {
+    const int b = tid * per + k;
+    const int n = b < a.B ? attn_units(a, b) : 1;
+    if (b < a.B) mine += n;
+    unsigned empty = __ballot_sync(0xffffffffu, n == 0 && b % gridDim.x == blockIdx.x);
     while (empty) {
-      const int b = b0 + __ffs(empty) - 1;
+      const int eb = __shfl_sync(0xffffffffu, b, __ffs(empty) - 1);
       empty &= empty - 1;
       for (int i = lane; i < a.q_heads * (D / 8); i += 32)
-        *reinterpret_cast<uint4 *>(a.out + b * a.os + (size_t)i * 8) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(a.out + eb * a.os + (size_t)i * 8) = make_uint4(0, 0, 0, 0);
       if (a.lse)
-        for (int i = lane; i < a.q_heads; i += 32) a.lse[(size_t)b * a.q_heads + i] = -INFINITY;
+        for (int i = lane; i < a.q_heads; i += 32) a.lse[(size_t)eb * a.q_heads + i] = -INFINITY;
     }
   }
-
-  // the line's length, and where each of this CTA's warps starts
-  const int per = (a.B + THREADS - 1) / THREADS;
-  const int bs = min(tid * per, a.B), be = min(bs + per, a.B);
-  long long mine = 0;
-  for (int b = bs; b < be; ++b) mine += attn_units(a, b);
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -295,34 +290,39 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + 32, 1) attn_ke
     if (w < warp) before += s_scan[w];
     sum += s_scan[w];
   }
+  head->before[tid] = before;
   const long long total = sum * items;
   const long long want = (total + W - 1) / W;  // a unit per warp at least
   const int ctas = (int)(want < gridDim.x ? want : gridDim.x);
   if ((int)blockIdx.x >= ctas) return;
   const long long c_begin = attn_div(blockIdx.x * total, ctas);
   const long long c_units = attn_div((blockIdx.x + 1) * total, ctas) - c_begin;
-  if (mine) {
-    for (int w = 0; w < W; ++w) {
-      const long long at = c_begin + w * c_units / W;
-      if (at < before * items || at >= (before + mine) * items) continue;
-      long long p = before * items;
-      int b = bs;
-      while (true) {
-        const long long n = (long long)attn_units(a, b) * items;
-        if (at < p + n) break;
-        p += n;
-        ++b;
-      }
-      s_start.b[w] = b;
-      s_start.off[w] = at - p;
-    }
-  }
+  // this warp's units (producer: lane w has warp w's)
+  const int wi = warp < W ? warp : min(lane, W);
+  const long long w_begin = wi * c_units / W;
+  int left = wi < W ? (int)((wi + 1) * c_units / W - w_begin) : 0;
   __syncthreads();
+  AttnWalk pw{};  // where they begin
+  if (left > 0) {
+    const long long at = c_begin + w_begin, seq = attn_div(at, items);
+    const int shares = (a.B + per - 1) / per;
+    int lo = 0;  // the last share that begins at or before `at`
+    for (int o = 1 << 8; o > 0; o >>= 1)
+      if (lo + o < shares && head->before[lo + o] <= seq) lo += o;
+    long long off = at - head->before[lo] * items;
+    for (pw.b = lo * per;; ++pw.b) {
+      pw.open(a);
+      const long long n = (long long)pw.nu * items;
+      if (off < n) break;
+      off -= n;
+    }
+    pw.it = (int)attn_div(off, pw.nu);
+    pw.u = (int)(off - (long long)pw.it * pw.nu);
+  }
 
   if (warp == W) {
     // The producer: lane w walks consumer warp w's part of the line.
-    AttnWalk pw{};
-    int to_issue = 0, issued = 0, stage = 0, pidx = 0, psub = 0, pg = 0;
+    int to_issue = left, issued = 0, stage = 0, pidx = 0, psub = 0, pg = 0;
     uint32_t parity = 1;
     const int upp = a.kv.page_units;
     auto locate = [&]() {
@@ -330,16 +330,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + 32, 1) attn_ke
       psub = (pw.u0 + pw.u) - pidx * upp;
       pg = a.page_table[(size_t)pw.b * a.max_pages + pidx];
     };
-    if (lane < W) {
-      to_issue = (int)((lane + 1) * c_units / W - lane * c_units / W);
-      if (to_issue > 0) {
-        pw.b = s_start.b[lane];
-        pw.open(a);
-        pw.it = (int)attn_div(s_start.off[lane], pw.nu);
-        pw.u = (int)(s_start.off[lane] - (long long)pw.it * pw.nu);
-        locate();
-      }
-    }
+    if (to_issue > 0) locate();
     unsigned long long idle = 0;
     while (__any_sync(0xffffffffu, to_issue > 0)) {
       const int slot = lane * STAGES + stage;
@@ -385,14 +376,12 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + 32, 1) attn_ke
       }
     }
   }
-  const long long w_begin = warp < W ? warp * c_units / W : 0;
-  int left = warp < W ? (int)((warp + 1) * c_units / W - w_begin) : 0;
-  if (left > 0) {
+  if (warp < W && left > 0) {
     long long pos = c_begin + w_begin;  // the next unit, along the line
     uint8_t *ring = smem + ATTN_HEAD + warp * (STAGES * UNIT);
     float *rec0 = near_record(warp);
-    AttnUnit cu{};          // the item at hand
-    long long item_start = 0;
+    AttnUnit cu{pw.b, pw.it, pw.u, pw.nu};  // the item at hand
+    long long item_start = pos - pw.u;
     uint32_t qf[NT][D / 16][2];  // B fragments of q: k = this lane's channels, n = head g
     float qc[NT][2];             // score multiplier of heads 2t, 2t + 1
     float o[NT][D / 16][4], l[NT][2], ref[NT][2], refv[NT][2];
@@ -402,23 +391,13 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + 32, 1) attn_ke
 
     while (left > 0) {
       const int slot = warp * STAGES + stage;
-      if (!__all_sync(0xffffffffu, mbar_wait(&head->full[slot], parity))) {
-        // gave up (recorded): stop the copies, and give those in flight time to land before the CTA goes
-        s_stop = 1;
-        for (int k = 0; k < STAGES; ++k) {
-          mbar_wait(&head->full[warp * STAGES + stage], parity, WAIT_LIMIT_NS / 100);
-          if (++stage == STAGES) {
-            stage = 0;
-            parity ^= 1u;
-          }
-        }
-        break;
-      }
-      const int meta = head->meta[slot];
-      if (fresh) {
+      auto arrived = [&]() { return __all_sync(0xffffffffu, mbar_wait(&head->full[slot], parity)); };
+      if (fresh) {  // the first item is known before its unit is here
         fresh = false;
-        cu = head->unit[slot];
-        item_start = pos - cu.u;
+        if (pos != c_begin + w_begin && arrived()) {
+          cu = head->unit[slot];
+          item_start = pos - cu.u;
+        }
         const int h = cu.it / a.hgroups, hg = cu.it % a.hgroups;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -477,6 +456,19 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + 32, 1) attn_ke
         }
       }
 
+      if (!arrived()) {
+        // gave up (recorded): stop the copies, and give those in flight time to land before the CTA goes
+        s_stop = 1;
+        for (int k = 0; k < STAGES; ++k) {
+          mbar_wait(&head->full[warp * STAGES + stage], parity, WAIT_LIMIT_NS / 100);
+          if (++stage == STAGES) {
+            stage = 0;
+            parity ^= 1u;
+          }
+        }
+        break;
+      }
+      const int meta = head->meta[slot];
       if (!(meta & ATTN_BAD)) {
         uint8_t *unit = ring + stage * UNIT;
         const uint4 *kv4 = reinterpret_cast<const uint4 *>(unit) + lane;
@@ -737,118 +729,149 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + 32, 1) attn_ke
   }
   __syncthreads();
 
-  // Join the parts that the CTA's warps left, in the order of the tokens: runs
-  // of segments of one item.
+  // Join the parts that the CTA's warps left.  Lane e of every warp has segment
+  // e in the order of the tokens; a run of segments up to the next that begins
+  // an item is one item's.
+  const int fl = lane < 2 * W ? head->seg[lane].flags : 0;
+  const unsigned present = __ballot_sync(0xffffffffu, fl & 1), begin = __ballot_sync(0xffffffffu, fl & 2),
+                 end = __ballot_sync(0xffffffffu, fl & 4), starts = begin | 1u;
   auto record = [&](int e) {
-    return e & 1 ? reinterpret_cast<const float *>(smem + ATTN_HEAD + (e >> 1) * (STAGES * UNIT))
-                 : near_record(e >> 1);
+    return e & 1 ? reinterpret_cast<const float *>(smem + ATTN_HEAD + (e >> 1) * (STAGES * UNIT)) : near_record(e >> 1);
   };
-  auto finish = [&](int b, int it, int hl, int d, float4 v, float lse2) {  // 4 channels of one head
-    const int hq = (it % a.hgroups) * GT + hl;
+  auto finish = [&](const AttnSeg &sg, int hl, int d, float4 v, float lse2) {  // 4 channels of one head
+    const int hq = (sg.it % a.hgroups) * GT + hl;
     if (hq >= a.group) return;
-    const size_t row = (size_t)(it / a.hgroups) * a.group + hq;
-    *reinterpret_cast<uint2 *>(a.out + b * a.os + row * D + d) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
-    if (a.lse && d == 0) a.lse[(size_t)b * a.q_heads + row] = lse2 * 0.6931471805599453f;
+    const size_t row = (size_t)(sg.it / a.hgroups) * a.group + hq;
+    *reinterpret_cast<uint2 *>(a.out + sg.b * a.os + row * D + d) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+    if (a.lse && d == 0) a.lse[(size_t)sg.b * a.q_heads + row] = lse2 * 0.6931471805599453f;
   };
-  int open = 0;  // records in the workspace: bit 0: of an item begun before, bit 1: of one that goes on
-  AttnSeg seg[2];
-  for (int e = 0; e < 2 * W;) {
-    const AttnSeg first = head->seg[e];
-    if (!first.flags) {
-      ++e;
-      continue;
+  // each segment's weight and each run's log2 sum, by scans within the runs
+  float *weight = reinterpret_cast<float *>(head->before), *run_lse = weight + GT * 32;  // [GT][32]
+  {
+    const unsigned upto = (2u << lane) - 1u, after = starts & ~upto;
+    const int run = 31 - __clz(starts & upto), run_end = after ? __ffs(after) - 2 : 31;
+    for (int hl = warp; hl < GT; hl += W + 1) {
+      const float ls = fl & 1 ? record(lane)[GT * D + hl * 4] : -INFINITY;
+      float m = ls;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float u = __shfl_up_sync(0xffffffffu, m, o);
+        if (lane - o >= run) m = fmaxf(m, u);
+      }
+      m = __shfl_sync(0xffffffffu, m, run_end);
+      const float r = m == -INFINITY ? 0.f : m, w = ex2(ls - r);
+      float s = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float u = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane - o >= run) s += u;
+      }
+      s = __shfl_sync(0xffffffffu, s, run_end);
+      weight[hl * 32 + lane] = s == 0.f ? 0.f : w / s;
+      if (lane == run) run_lse[hl * 32 + lane] = s == 0.f ? -INFINITY : r + lg2(s);
     }
-    int last = e, next = e + 1;
-    for (; next < 2 * W; ++next) {
-      if (!head->seg[next].flags) continue;
-      if (head->seg[next].start != first.start) break;
-      last = next;
-    }
-    const bool begins = first.flags & 2, ends = head->seg[last].flags & 4;
-    float *to = a.parts + ((size_t)blockIdx.x * 2 + (begins ? 1 : 0)) * (PART / 4);
+  }
+  __syncthreads();
+  // Records that stay in the workspace: [0] of an item begun before this CTA,
+  // [1] of one that goes on after it.
+  int open0 = -1, open1 = -1;  // a segment of theirs
+  for (unsigned todo = starts; todo; todo &= todo - 1) {
+    const int e0 = __ffs(todo) - 1;
+    const unsigned next = todo & (todo - 1);
+    const unsigned members = present & ~((1u << e0) - 1u) & (next ? (next & -next) - 1u : ~0u);
+    if (!members) continue;
+    const int first = __ffs(members) - 1;
+    const bool begins = begin >> e0 & 1u, ends = end & members;
+    const AttnSeg sg = head->seg[first];
+    float *to = a.parts + ((size_t)blockIdx.x * 2 + begins) * (PART / 4);
     for (int x = tid; x < GT * D / 4; x += THREADS) {
       const int hl = x / (D / 4), d = (x % (D / 4)) * 4;
-      float m = -INFINITY, s = 0.f;
-      for (int i = e; i <= last; ++i)
-        if (head->seg[i].flags) m = fmaxf(m, record(i)[GT * D + hl * 4]);
-      const float r = m == -INFINITY ? 0.f : m;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i = e; i <= last; ++i) {
-        if (!head->seg[i].flags) continue;
-        const float *rec = record(i);
-        const float w = ex2(rec[GT * D + hl * 4] - r);
-        const float4 p = *reinterpret_cast<const float4 *>(rec + hl * D + d);
-        s += w;
-        v.x += w * p.x; v.y += w * p.y; v.z += w * p.z; v.w += w * p.w;
+      for (unsigned mm = members; mm;) {
+        float w[4];
+        float4 p[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int e = mm ? __ffs(mm) - 1 : first;
+          w[k] = mm ? weight[hl * 32 + e] : 0.f;
+          p[k] = *reinterpret_cast<const float4 *>(record(e) + hl * D + d);
+          mm &= mm - 1;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v.x += w[k] * p[k].x; v.y += w[k] * p[k].y; v.z += w[k] * p[k].z; v.w += w[k] * p[k].w;
+        }
       }
-      const float inv = s == 0.f ? 0.f : 1.f / s, lse2 = s == 0.f ? -INFINITY : r + lg2(s);
-      v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
+      const float lse2 = run_lse[hl * 32 + e0];
       if (begins && ends) {
-        finish(first.b, first.it, hl, d, v, lse2);
+        finish(sg, hl, d, v, lse2);
       } else {
         __stcg(reinterpret_cast<float4 *>(to + hl * D + d), v);
         if (d == 0) __stcg(to + GT * D + hl * 4, lse2);
       }
     }
-    if (!(begins && ends)) {
-      open |= begins ? 2 : 1;
-      seg[begins ? 1 : 0] = first;
-    }
-    e = next;
+    if (!(begins && ends)) (begins ? open1 : open0) = first;
   }
-  if (!open) return;
+  if (open0 < 0 && open1 < 0) return;
 
   // Items that span CTAs: the last CTA to arrive joins their records.  The
   // counter is that of the CTA in which the item begins.
-  __threadfence();
   __syncthreads();
-  if (tid < 2) {
-    s_last[tid] = 0;
-    if (open >> tid & 1) {
-      const long long start = seg[tid].start;
-      const int c0 = attn_cta_of(start, total, ctas), c1 = attn_cta_of(start + seg[tid].nu - 1, total, ctas);
-      if (atomicAdd(&a.counters[c0], 1) == c1 - c0) {
-        a.counters[c0] = 0;
-        s_last[tid] = 1;
+  if (tid == 0) {
+    __threadfence();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int e = k ? open1 : open0;
+      int last = 0;
+      if (e >= 0) {
+        const AttnSeg sg = head->seg[e];
+        const int c0 = attn_cta_of(sg.start, total, ctas), c1 = attn_cta_of(sg.start + sg.nu - 1, total, ctas);
+        s_from[k] = c0;
+        s_from[2 + k] = c1 - c0 + 1;
+        if (atomicAdd(&a.counters[c0], 1) == c1 - c0) {
+          a.counters[c0] = 0;
+          last = 1;
+        }
       }
-      __threadfence();
+      s_last[k] = last;
     }
+    __threadfence();
   }
   __syncthreads();
   for (int k = 0; k < 2; ++k) {
     if (!s_last[k]) continue;
-    const int c0 = attn_cta_of(seg[k].start, total, ctas);
-    const int n = attn_cta_of(seg[k].start + seg[k].nu - 1, total, ctas) - c0 + 1;
-    // the records: c0's is of an item begun there, the others' of one begun before
-    const float *recs = a.parts + (size_t)c0 * 2 * (PART / 4);
+    const AttnSeg sg = head->seg[k ? open1 : open0];
+    const int n = s_from[2 + k];
+    // the records: that of the CTA in which the item begins, then the others'
+    const float *recs = a.parts + (size_t)s_from[k] * 2 * (PART / 4);
     auto rec = [&](int c) { return recs + ((size_t)c * 2 + (c == 0 ? 1 : 0)) * (PART / 4); };
-    float *weight = reinterpret_cast<float *>(smem + ATTN_HEAD);  // [GT][n], where the rings were
-    for (int i = tid; i < GT * n; i += THREADS) weight[i] = __ldcg(rec(i % n) + GT * D + i / n * 4);
+    float *w = reinterpret_cast<float *>(smem + ATTN_HEAD);  // [n][GT], where the rings were
+    for (int i = tid; i < GT * n; i += THREADS) w[i] = __ldcg(rec(i / GT) + GT * D + i % GT * 4);
     __syncthreads();
     for (int hl = warp; hl < GT; hl += W + 1) {
       float m = -INFINITY, s = 0.f;
-      for (int c = lane; c < n; c += 32) m = fmaxf(m, weight[hl * n + c]);
+      for (int c = lane; c < n; c += 32) m = fmaxf(m, w[c * GT + hl]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       const float r = m == -INFINITY ? 0.f : m;
-      for (int c = lane; c < n; c += 32) s += ex2(weight[hl * n + c] - r);
+      for (int c = lane; c < n; c += 32) s += ex2(w[c * GT + hl] - r);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       const float inv = s == 0.f ? 0.f : 1.f / s;
-      for (int c = lane; c < n; c += 32) weight[hl * n + c] = ex2(weight[hl * n + c] - r) * inv;
+      for (int c = lane; c < n; c += 32) w[c * GT + hl] = ex2(w[c * GT + hl] - r) * inv;
       if (lane == 0) s_lse[hl] = s == 0.f ? -INFINITY : r + lg2(s);
     }
     __syncthreads();
     for (int x = tid; x < GT * D / 4; x += THREADS) {
       const int hl = x / (D / 4), d = (x % (D / 4)) * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 16
       for (int c = 0; c < n; ++c) {
-        const float w = weight[hl * n + c];
+        const float wc = w[c * GT + hl];
         const float4 p = __ldcg(reinterpret_cast<const float4 *>(rec(c) + hl * D + d));
-        v.x += w * p.x; v.y += w * p.y; v.z += w * p.z; v.w += w * p.w;
+        v.x += wc * p.x; v.y += wc * p.y; v.z += wc * p.z; v.w += wc * p.w;
       }
-      finish(seg[k].b, seg[k].it, hl, d, v, s_lse[hl]);
+      finish(sg, hl, d, v, s_lse[hl]);
     }
     __syncthreads();
   }
