@@ -754,8 +754,8 @@ hq_status hq_rope(const hq_rope_desc *rope, int T, int H, int D, const void *x_b
   if (x_bf16 == out_bf16 && (x_token_stride != out_token_stride || x_head_stride != out_head_stride))
     return HQ_ERR_INVALID_ARG;
   if (!device_is_sm100()) return HQ_ERR_ARCH;
-  const RopeArgs a{T, H, D, rope->rot_dim, rope->interleaved, P, (const uint16_t *)x_bf16, x_token_stride,
-                   x_head_stride, positions, table, (uint16_t *)out_bf16, out_token_stride, out_head_stride};
+  const RopeArgs a = rope_args(T, H, D, rope, P, x_bf16, x_token_stride, x_head_stride, positions, table, out_bf16,
+                               out_token_stride, out_head_stride, ROPE_THREADS);
   return launch_rope(a, (cudaStream_t)stream);
 }
 
@@ -796,10 +796,8 @@ static hq_status kv_write(const hq_rope_desc *rope, const hq_kv_desc *kv, int T,
   w.vs = v_stride;
   w.slots = (const long long *)slots;
   RopeArgs r{};
-  if (rope) {
-    r = RopeArgs{T, q_heads, D, rope->rot_dim, rope->interleaved, P, (const uint16_t *)q, q_stride, D,
-                 positions, table, (uint16_t *)q_out, q_out_stride, D};
-  }
+  if (rope)
+    r = rope_args(T, q_heads, D, rope, P, q, q_stride, D, positions, table, q_out, q_out_stride, D, KV_THREADS);
   return launch_kv_write(fmt, D, a, w, r, (cudaStream_t)stream);
 }
 

@@ -18,6 +18,7 @@
 // Scales: E4M3 fp32 [16 tokens] for K, then V; NVFP4 K [16 tokens][2][D / 32]
 // (16-channel block 2b + h at [h][b]), V [D / 16 blocks][16 tokens].
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <type_traits>
 
@@ -48,27 +49,49 @@ __device__ __forceinline__ double rope_freq(const hq_rope_desc &d, int i) {
   return f;
 }
 
+// Sine and cosine of |r| <= pi / 4 by their Taylor sums, to r^9 and r^10: what
+// is left out is under 2e-9, a thirtieth of an fp32 step.
+__device__ __forceinline__ void sincos_small(float r, float &s, float &c) {
+  const float z = r * r;
+  s = fmaf(fmaf(fmaf(fmaf(z, 1.f / 362880.f, -1.f / 5040.f), z, 1.f / 120.f), z, -1.f / 6.f), z * r, r);
+  c = fmaf(fmaf(fmaf(fmaf(fmaf(z, -1.f / 3628800.f, 1.f / 40320.f), z, -1.f / 720.f), z, 1.f / 24.f), z, -0.5f), z, 1.f);
+}
+
 // table[p] = amplitude * (cos(p f_0) .. cos(p f_{R/2-1}), sin(p f_0) ..).  The
 // angle of a far position does not fit fp32 (position 131072 leaves 2^-7 of a
 // radian there), so the product and the reduction are 64-bit: the angle is
-// counted in turns and brought to [-1/8, 1/8] of one; what is left is at most
-// pi/4 and goes through fp32 sine and cosine, an error of about one fp32 step.
-__global__ void rope_table_kernel(hq_rope_desc d, long long P, float *__restrict__ table) {
+// counted in turns and brought to [-1/8, 1/8] of one; what is left goes
+// through fp32 sums, an error of about one fp32 step.  Bound by its stores:
+// 131072 x 128 (67 MB) in TABLE_LONG us of a floor of 10 (library sine and
+// cosine, two warps a block: 32).
+constexpr int TABLE_THREADS = 256;
+__global__ void __launch_bounds__(TABLE_THREADS) rope_table_kernel(hq_rope_desc d, long long P, float *__restrict__ table) {
+  __shared__ double per[512];  // turns per position
   const int half = d.rot_dim / 2;
   const float amp = (float)d.amplitude;
-  for (int i = threadIdx.x; i < half; i += blockDim.x) {
-    const double per = rope_freq(d, i) / 6.283185307179586476925;  // turns per position
-    for (long long p = blockIdx.x; p < P; p += gridDim.x) {
-      const double turns = (double)p * per;
+  for (int i = threadIdx.x; i < half; i += TABLE_THREADS) per[i] = rope_freq(d, i) / 6.283185307179586476925;
+  __syncthreads();
+  // threads of a block: `cols` frequencies (all, up to the block's width) x rows
+  const int cols = min(half, TABLE_THREADS), rows = TABLE_THREADS / cols;
+  const int row = threadIdx.x / cols;
+  if (row >= rows) return;
+  for (int i = threadIdx.x - row * cols; i < half; i += cols) {
+    const double f = per[i];
+    const long long step = (long long)gridDim.x * rows;
+#pragma unroll 4
+    for (long long p = blockIdx.x * (long long)rows + row; p < P; p += step) {
+      const double turns = (double)p * f;
       const double quarters = rint(turns * 4.0);
       const float r = (float)((turns - quarters * 0.25) * 6.283185307179586476925);
       const int quad = (int)((long long)quarters & 3);
-      const float s = sinf(r), c = cosf(r);
+      float s, c;
+      sincos_small(r, s, c);
       float co = (quad & 1) ? s : c, si = (quad & 1) ? c : s;
       if (quad == 1 || quad == 2) co = -co;
       if (quad >= 2) si = -si;
-      table[p * d.rot_dim + i] = amp * co;
-      table[p * d.rot_dim + half + i] = amp * si;
+      float *to = table + p * d.rot_dim + i;
+      to[0] = amp * co;
+      to[half] = amp * si;
     }
   }
 }
@@ -76,11 +99,9 @@ __global__ void rope_table_kernel(hq_rope_desc d, long long P, float *__restrict
 hq_status launch_rope_table(const hq_rope_desc *d, int P, float *table, cudaStream_t st) {
   hq_rope_desc r = *d;
   if (r.amplitude == 0.0) r.amplitude = 1.0;
-  const int half = r.rot_dim / 2;
-  int threads = (half + 31) / 32 * 32;
-  if (threads > 256) threads = 256;
-  const int blocks = P < 148 * 8 ? P : 148 * 8;
-  rope_table_kernel<<<blocks, threads, 0, st>>>(r, P, table);
+  const int half = r.rot_dim / 2, rows = TABLE_THREADS / (half < TABLE_THREADS ? half : TABLE_THREADS);
+  const int want = (P + rows - 1) / rows;
+  rope_table_kernel<<<want < 148 * 8 ? want : 148 * 8, TABLE_THREADS, 0, st>>>(r, P, table);
   return check_launch();
 }
 
@@ -113,44 +134,66 @@ __device__ __forceinline__ void load8(const float *p, float *f) {
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
-// Work of a head: chunks of 8 pairs, then chunks of 8 unrotated channels.  A
+// Work of a head: chunks of 8 pairs, then chunks of 16 unrotated channels (the
+// last may have 8 or, where pairs straddle 16-byte pieces, any number).  A
 // chunk holds both channels of its pairs, so x and out may be the same.
-// Widths that are a multiple of 16 move 16 bytes at a time; others (pairs
-// that straddle 16-byte pieces) go channel by channel.
-__host__ __device__ inline int rope_chunks(int D, int rot) { return (rot / 2 + 7) / 8 + (D - rot + 7) / 8; }
+__host__ __device__ inline int rope_chunks(int D, int rot) { return (rot / 2 + 7) / 8 + (D - rot + 15) / 16; }
 
-__device__ __forceinline__ void rope_chunk(int c, int D, int rot, int inter, const uint16_t *x,
-                                           const float *tab, uint16_t *out) {
-  const int half = rot / 2, npair = (half + 7) / 8;
-  if (c >= npair) {  // past the rotated part: copied
-    if (x == out) return;
-    const int ch = rot + (c - npair) * 8;
-    if ((rot & 7) == 0) {
-      *reinterpret_cast<uint4 *>(out + ch) = *reinterpret_cast<const uint4 *>(x + ch);
-    } else {
-      for (int i = ch; i < ch + 8 && i < D; ++i) out[i] = x[i];
-    }
+// rot_dim a multiple of 16: a chunk is two 16-byte pieces (the second may be
+// missing), loaded before anything that depends on the position.
+struct RopePiece {
+  const uint16_t *x;  // the head's row, or null: no chunk
+  uint16_t *out;
+  long long t;
+  int c;
+  uint4 a, b;
+};
+__device__ __forceinline__ void rope_where(const RopePiece &r, int D, int rot, int inter, int &i0, int &i1, bool &pair) {
+  const int half = rot / 2, npair = half / 8;
+  pair = r.c < npair;
+  if (pair) {
+    i0 = inter ? 16 * r.c : 8 * r.c;
+    i1 = inter ? i0 + 8 : i0 + half;
+  } else {
+    i0 = rot + 16 * (r.c - npair);
+    i1 = i0 + 8 < D ? i0 + 8 : -1;
+  }
+}
+__device__ __forceinline__ void rope_piece(const RopePiece &r, int D, int rot, int inter, const float *tab) {
+  int i0, i1;
+  bool pair;
+  rope_where(r, D, rot, inter, i0, i1, pair);
+  if (!pair) {
+    if (r.x == r.out) return;
+    *reinterpret_cast<uint4 *>(r.out + i0) = r.a;
+    if (i1 >= 0) *reinterpret_cast<uint4 *>(r.out + i1) = r.b;
     return;
   }
-  if ((rot & 15) == 0) {
-    const int i0 = inter ? 16 * c : 8 * c, i1 = inter ? 16 * c + 8 : 8 * c + half;
-    float a[8], b[8], co[8], si[8];
-    unpack8(*reinterpret_cast<const uint4 *>(x + i0), a);
-    unpack8(*reinterpret_cast<const uint4 *>(x + i1), b);
-    load8(tab + 8 * c, co);
-    load8(tab + half + 8 * c, si);
-    if (inter) {
+  float a[8], b[8], co[8], si[8];
+  unpack8(r.a, a);
+  unpack8(r.b, b);
+  load8(tab + 8 * r.c, co);
+  load8(tab + rot / 2 + 8 * r.c, si);
+  if (inter) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        rope_pair(a[2 * j], a[2 * j + 1], co[j], si[j], a[2 * j], a[2 * j + 1]);
-        rope_pair(b[2 * j], b[2 * j + 1], co[4 + j], si[4 + j], b[2 * j], b[2 * j + 1]);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) rope_pair(a[j], b[j], co[j], si[j], a[j], b[j]);
+    for (int j = 0; j < 4; ++j) {
+      rope_pair(a[2 * j], a[2 * j + 1], co[j], si[j], a[2 * j], a[2 * j + 1]);
+      rope_pair(b[2 * j], b[2 * j + 1], co[4 + j], si[4 + j], b[2 * j], b[2 * j + 1]);
     }
-    *reinterpret_cast<uint4 *>(out + i0) = pack8(a);
-    *reinterpret_cast<uint4 *>(out + i1) = pack8(b);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rope_pair(a[j], b[j], co[j], si[j], a[j], b[j]);
+  }
+  *reinterpret_cast<uint4 *>(r.out + i0) = pack8(a);
+  *reinterpret_cast<uint4 *>(r.out + i1) = pack8(b);
+}
+
+// Other widths, channel by channel.
+__device__ __noinline__ void rope_slow(int c, int D, int rot, int inter, const uint16_t *x, const float *tab, uint16_t *out) {
+  const int half = rot / 2, npair = (half + 7) / 8;
+  if (c >= npair) {
+    const int ch = rot + (c - npair) * 16;
+    for (int i = ch; i < ch + 16 && i < D; ++i) out[i] = x[i];
     return;
   }
   for (int i = 8 * c; i < 8 * c + 8 && i < half; ++i) {
@@ -162,6 +205,19 @@ __device__ __forceinline__ void rope_chunk(int c, int D, int rot, int inter, con
   }
 }
 
+// n / d for n < 2^31 by a product: q = (umulhi(n, m) + n) >> s with
+// s = ceil(log2 d), m = floor(2^32 (2^s - d) / d) + 1.
+struct FastDiv {
+  uint32_t d, m;
+  int s;
+};
+static FastDiv fast_div(uint32_t d) {
+  int s = 0;
+  while ((1ull << s) < d) ++s;
+  return FastDiv{d, (uint32_t)(((((1ull << s) - d) << 32) / d) + 1), s};
+}
+__device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv &f) { return (__umulhi(n, f.m) + n) >> f.s; }
+
 struct RopeArgs {
   int T, H, D, rot, inter, P;
   const uint16_t *x;
@@ -170,33 +226,80 @@ struct RopeArgs {
   const float *table;
   uint16_t *out;
   long long ot, oh;
+  FastDiv chunks, per_token;  // chunks of a head and of a token
+  FastDiv parts;              // blocks of a token
+  int tokens;                 // tokens of a block
 };
 
-__device__ __forceinline__ void rope_rows(const RopeArgs &a, size_t first, size_t step) {
-  const int nc = rope_chunks(a.D, a.rot);
-  const size_t total = (size_t)a.T * a.H * nc;
-  for (size_t i = first; i < total; i += step) {
-    const int c = (int)(i % nc);
-    const size_t th = i / nc;
-    const int h = (int)(th % a.H);
-    const size_t t = th / a.H;
-    const int p = a.pos[t];
+// A block has up to ROPE_EACH chunks a thread: several whole tokens, or one of
+// `parts` parts of a token.
+constexpr int ROPE_EACH = 2;
+struct RopeSplit {
+  int tokens, parts;
+};
+inline RopeSplit rope_split(int T, int per_token, int threads) {
+  const int full = ROPE_EACH * threads;
+  int n = full / per_token;
+  if (n > T / (148 * 4)) n = T / (148 * 4);  // blocks enough for every SM come first
+  return RopeSplit{n > 1 ? n : 1, (per_token + full - 1) / full};
+}
+inline long long rope_blocks(const RopeArgs &a) { return ((long long)a.T + a.tokens - 1) / a.tokens * a.parts.d; }
+
+// Bound by HBM: x is read and out written once, the table rows come from L2
+// (one of a token for all of its heads).  8191 tokens x 32 heads x 192 (a third rotated):
+// ROPE_PROMPT us, ROPE_RATE TB/s of the measured 6.55.
+__device__ __forceinline__ void rope_rows(const RopeArgs &a, uint32_t block) {
+  const uint32_t tb = div_by(block, a.parts), part = block - tb * a.parts.d;
+  const long long t0 = (long long)tb * a.tokens;
+  const uint32_t n = (uint32_t)min((long long)a.tokens, a.T - t0) * a.per_token.d;
+  const uint32_t i0 = part * ROPE_EACH * blockDim.x + threadIdx.x;
+  const bool fast = (a.rot & 15) == 0;
+  RopePiece r[ROPE_EACH];
+#pragma unroll
+  for (int u = 0; u < ROPE_EACH; ++u) {
+    const uint32_t i = i0 + u * blockDim.x;
+    r[u].x = nullptr;
+    if (i >= n) continue;
+    const uint32_t tt = div_by(i, a.per_token), in = i - tt * a.per_token.d, h = div_by(in, a.chunks);
+    r[u].c = in - h * a.chunks.d;
+    r[u].t = t0 + tt;
+    r[u].x = a.x + r[u].t * a.xt + h * a.xh;
+    r[u].out = a.out + r[u].t * a.ot + h * a.oh;
+    if (!fast) continue;
+    int p0, p1;
+    bool pair;
+    rope_where(r[u], a.D, a.rot, a.inter, p0, p1, pair);
+    if (!pair && r[u].x == r[u].out) continue;
+    r[u].a = *reinterpret_cast<const uint4 *>(r[u].x + p0);
+    if (p1 >= 0) r[u].b = *reinterpret_cast<const uint4 *>(r[u].x + p1);
+  }
+#pragma unroll
+  for (int u = 0; u < ROPE_EACH; ++u) {
+    if (!r[u].x) continue;
+    const int p = a.pos[r[u].t];
     if (p < 0 || p >= a.P) {
       set_device_error(HQ_ERR_DEVICE_INDEX);
       continue;
     }
-    rope_chunk(c, a.D, a.rot, a.inter, a.x + t * a.xt + h * a.xh, a.table + (size_t)p * a.rot,
-               a.out + t * a.ot + h * a.oh);
+    const float *tab = a.table + (size_t)p * a.rot;
+    if (fast) rope_piece(r[u], a.D, a.rot, a.inter, tab);
+    else rope_slow(r[u].c, a.D, a.rot, a.inter, r[u].x, tab, r[u].out);
   }
 }
 
-__global__ void rope_kernel(RopeArgs a) {
-  rope_rows(a, blockIdx.x * (size_t)blockDim.x + threadIdx.x, (size_t)gridDim.x * blockDim.x);
+constexpr int ROPE_THREADS = 256;
+__global__ void __launch_bounds__(ROPE_THREADS, 4) rope_kernel(RopeArgs a) { rope_rows(a, blockIdx.x); }
+
+RopeArgs rope_args(int T, int H, int D, const hq_rope_desc *r, int P, const void *x, int64_t xt, int64_t xh,
+                   const int32_t *pos, const float *table, void *out, int64_t ot, int64_t oh, int threads) {
+  const int nc = rope_chunks(D, r->rot_dim), per_token = nc * (H > 0 ? H : 1);
+  const RopeSplit split = rope_split(T, per_token, threads);
+  return RopeArgs{T, H, D, r->rot_dim, r->interleaved, P, (const uint16_t *)x, xt, xh, pos, table, (uint16_t *)out,
+                  ot, oh, fast_div(nc), fast_div(per_token), fast_div(split.parts), split.tokens};
 }
 
 hq_status launch_rope(const RopeArgs &a, cudaStream_t st) {
-  const size_t total = (size_t)a.T * a.H * rope_chunks(a.D, a.rot);
-  rope_kernel<<<quant_grid(total, 256), 256, 0, st>>>(a);
+  rope_kernel<<<(unsigned)rope_blocks(a), ROPE_THREADS, 0, st>>>(a);
   return check_launch();
 }
 
@@ -231,114 +334,62 @@ struct KvArgs {
   const float *glob;        // NVFP4: second-level scales of K and V
 };
 
-// The unit and the row inside it of (slot, head).
-template <int FMT, int D>
-__device__ __forceinline__ uint8_t *kv_unit(const KvArgs &a, long long slot, int h, int &r) {
-  const long long pg = slot / a.page;
-  const int off = (int)(slot - pg * a.page);
-  r = off & 15;
-  return a.pages + (size_t)pg * a.page_bytes + ((size_t)h * a.page_units + (off >> 4)) * kv_unit_bytes(FMT, D);
-}
-
-// Stores octet o of a token's key (IS_V = 0) or value.  The LPR lanes of a
-// row call it together (`on`: the lane has an octet; D = 192 leaves a quarter
-// of its 32 lanes idle).
-template <int FMT, int D, int LPR>
-__device__ __forceinline__ void kv_store(uint8_t *unit, int r, int o, bool on, bool is_v, const float *f,
-                                         const float *glob) {
-  constexpr int GS = kv_granule(FMT), CB = kv_code_bytes(FMT, D), SB = kv_scale_bytes(FMT, D);
-  uint8_t *codes = unit + (is_v ? CB : 0) + (is_v ? v_octet<GS, D>(o, r) : k_octet<GS>(o, r));
-  if constexpr (FMT == A_BF16) {
-    if (on) *reinterpret_cast<uint4 *>(codes) = pack8(f);
-  } else {
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
-    uint8_t *scales = unit + 2 * CB + (is_v ? SB : 0);
-    if constexpr (FMT == A_FP8) {
-      // hq_quant_act's per-token recipe on the head's D channels
-#pragma unroll
-      for (int k = LPR / 2; k > 0; k >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, k));
-      const float s = (amax == 0.f) ? 1.f : __fdiv_rn(amax, 448.f);
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = f32x2_to_e4m3x2(__fdiv_rn(f[2 * i], s), __fdiv_rn(f[2 * i + 1], s));
-      if (on) *reinterpret_cast<uint2 *>(codes) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-      if (on && o == 0) reinterpret_cast<float *>(scales)[r] = s;
-    } else {
-      // hq_quant_act's NVFP4 recipe with a static tensor scale; a block is two lanes
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      const float g = glob[is_v ? 1 : 0];
-      const uint32_t sb = f32x2_to_e4m3x2(__fdiv_rn(__fdiv_rn(amax, 6.f), g), 0.f) & 0xFFu;
-      const float d = __fmul_rn(e4m3_to_f32(sb), g);
-      uint32_t w = 0;
-      if (d != 0.f) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w |= f32x2_to_e2m1x2(__fdiv_rn(f[2 * i], d), __fdiv_rn(f[2 * i + 1], d)) << (8 * i);
-      }
-      if (on) {
-        *reinterpret_cast<uint32_t *>(codes) = w;
-        const int b = o >> 1;
-        if ((o & 1) == 0) scales[is_v ? b * 16 + r : r * (D / 16) + (b & 1) * (D / 32) + (b >> 1)] = (uint8_t)sb;
-      }
-    }
-  }
-}
-
-// Octet o of a token's key or value as fp32.
-template <int FMT, int D>
-__device__ __forceinline__ void kv_load(const uint8_t *unit, int r, int o, bool is_v, const float *glob, float *f) {
-  constexpr int GS = kv_granule(FMT), CB = kv_code_bytes(FMT, D), SB = kv_scale_bytes(FMT, D);
-  const uint8_t *codes = unit + (is_v ? CB : 0) + (is_v ? v_octet<GS, D>(o, r) : k_octet<GS>(o, r));
-  const uint8_t *scales = unit + 2 * CB + (is_v ? SB : 0);
-  if constexpr (FMT == A_BF16) {
-    unpack8(*reinterpret_cast<const uint4 *>(codes), f);
-  } else if constexpr (FMT == A_FP8) {
-    const uint2 w = *reinterpret_cast<const uint2 *>(codes);
-    const float s = reinterpret_cast<const float *>(scales)[r];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(e4m3_to_f32(((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 0xFFu), s);
-  } else {
-    const uint32_t w = *reinterpret_cast<const uint32_t *>(codes);
-    const int b = o >> 1;
-    const float s = e4m3_to_f32(scales[is_v ? b * 16 + r : r * (D / 16) + (b & 1) * (D / 32) + (b >> 1)]);
-    const float g = glob[is_v ? 1 : 0];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(__fmul_rn(e2m1_to_f32((w >> (4 * i)) & 15u), s), g);
-  }
-}
-
-// Eight channels from octet o of a row, rotated (rot > 0) in fp32.
-__device__ __forceinline__ void rope_octet(const uint16_t *x, int o, int rot, int inter, const float *tab, float *f) {
-  unpack8(*reinterpret_cast<const uint4 *>(x + 8 * o), f);
+// Octet o of a row, rotated in fp32; any width, channel by channel.
+__device__ __noinline__ void rope_octet_slow(const uint16_t *x, int o, int rot, int inter, const float *tab, float *f) {
   const int half = rot / 2;
-  if (8 * o >= rot) return;
-  if ((rot & 15) == 0 && !inter) {
-    const bool second = 8 * o >= half;
-    float p[8], co[8], si[8], u;
-    unpack8(*reinterpret_cast<const uint4 *>(x + (second ? 8 * o - half : 8 * o + half)), p);
-    const float *t = tab + (second ? 8 * o - half : 8 * o);
-    load8(t, co);
-    load8(t + half, si);
+  for (int i = 0; i < 8; ++i) {
+    const int ch = 8 * o + i;
+    f[i] = bf16_at(x + ch);
+    if (ch >= rot) continue;
+    const int j = inter ? ch >> 1 : (ch < half ? ch : ch - half);
+    const bool second = inter ? (ch & 1) : ch >= half;
+    const float other = bf16_at(x + (inter ? ch ^ 1 : second ? ch - half : ch + half));
+    float u;
+    if (second) rope_pair(other, f[i], tab[j], tab[half + j], u, f[i]);
+    else rope_pair(f[i], other, tab[j], tab[half + j], f[i], u);
+  }
+}
+
+// A lane's octets 4 b + t of a row, rotated in fp32.
+template <int NB>
+__device__ __forceinline__ void rope_octets(const uint16_t *x, int t, int rot, int inter, const float *tab, float (&f)[NB][8]) {
+  const int half = rot / 2;
+  if (rot & 15) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (second) rope_pair(p[i], f[i], co[i], si[i], u, f[i]);
-      else rope_pair(f[i], p[i], co[i], si[i], f[i], u);
+    for (int b = 0; b < NB; ++b) {
+      float tmp[8];
+      rope_octet_slow(x, 4 * b + t, rot, inter, tab, tmp);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[b][i] = tmp[i];
     }
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int ch = 8 * o + i;
-    if (ch >= rot) break;
-    const int j = inter ? ch >> 1 : (ch < half ? ch : ch - half);
-    const bool second = inter ? (ch & 1) : ch >= half;
-    const float mine = bf16_at(x + ch), other = bf16_at(x + (inter ? ch ^ 1 : second ? ch - half : ch + half));
-    float u, v;
-    if (second) rope_pair(other, mine, tab[j], tab[half + j], u, v);
-    else rope_pair(mine, other, tab[j], tab[half + j], v, u);
-    f[i] = v;
+  for (int b = 0; b < NB; ++b) unpack8(*reinterpret_cast<const uint4 *>(x + 32 * b + 8 * t), f[b]);
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int ch = 32 * b + 8 * t;
+    if (ch >= rot) continue;
+    if (inter) {  // the pairs are within the octet
+      const float4 co = *reinterpret_cast<const float4 *>(tab + ch / 2), si = *reinterpret_cast<const float4 *>(tab + half + ch / 2);
+      rope_pair(f[b][0], f[b][1], co.x, si.x, f[b][0], f[b][1]);
+      rope_pair(f[b][2], f[b][3], co.y, si.y, f[b][2], f[b][3]);
+      rope_pair(f[b][4], f[b][5], co.z, si.z, f[b][4], f[b][5]);
+      rope_pair(f[b][6], f[b][7], co.w, si.w, f[b][6], f[b][7]);
+    } else {
+      const bool second = ch >= half;
+      const int j = second ? ch - half : ch;
+      float p[8], co[8], si[8];
+      unpack8(*reinterpret_cast<const uint4 *>(x + (second ? j : ch + half)), p);
+      load8(tab + j, co);
+      load8(tab + half + j, si);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // a c - b s for the first of a pair, b c + a s for the second
+        const float u = __fmul_rn(f[b][i], co[i]), v = __fmul_rn(p[i], si[i]);
+        f[b][i] = second ? __fadd_rn(u, v) : __fsub_rn(u, v);
+      }
+    }
   }
 }
 
@@ -350,85 +401,494 @@ struct KvRows {
   uint16_t *k_out, *v_out;  // read back
 };
 
-template <int D>
-__host__ __device__ constexpr int kv_lpr() { return D == 64 ? 8 : D == 128 ? 16 : 32; }
+// A warp writes (reads) 16 consecutive tokens of the call and one head, its
+// lanes in the layout's own order: lane (g, t) = 4 g + t has octets 4 b + t of
+// keys g and g + 8 and octets g (D / 64) + q of values 2t, 2t + 1, 2t + 8,
+// 2t + 9, which are exactly the 16-byte vectors it holds in a unit.  Where the
+// tokens' slots run through one unit, or through the end of one and the
+// beginning of another (a prompt: rows r0, r0 + 1, .. modulo 16), lanes go by
+// the row in the unit and move whole vectors (split where their octets are in
+// two units); other groups (a decoding step's tokens) go by the token and move
+// octet by octet.  No shared memory, no barrier.
+constexpr int KV_THREADS = 64;
 
-// LPR lanes per (token, head): each takes one octet of the key and one of the
-// value.  Blocks past `kv_blocks` rotate the rope.H heads of q.
+struct KvGroup {
+  long long unit;  // lane i (and i + 16): byte offset of token i's unit (head 0), -1: none
+  int row;
+  bool run;
+  int r0;
+};
+
 template <int FMT, int D>
-__global__ void __launch_bounds__(256) kv_write_kernel(KvArgs a, KvRows w, RopeArgs rope, int kv_blocks) {
-  if (blockIdx.x >= kv_blocks) {
-    rope_rows(rope, (blockIdx.x - kv_blocks) * (size_t)blockDim.x + threadIdx.x,
-              (size_t)(gridDim.x - kv_blocks) * blockDim.x);
-    return;
-  }
-  constexpr int LPR = kv_lpr<D>();
-  const int o = threadIdx.x % LPR;
-  const bool on = o < D / 8;
-  const size_t rows = (size_t)w.T * a.H, step = (size_t)kv_blocks * (256 / LPR);
-  // whole warps stay together for the shuffles: a row past the end is clamped and not stored
-  for (size_t base = blockIdx.x * (size_t)(256 / LPR); base < rows; base += step) {
-    const size_t row = base + threadIdx.x / LPR;
-    const size_t t = (row < rows ? row : rows - 1) / a.H;
-    const int h = (int)((row < rows ? row : rows - 1) % a.H);
+__device__ __forceinline__ KvGroup kv_group(const KvArgs &a, const KvRows &w, const RopeArgs *rope, long long t0) {
+  const int i = threadIdx.x & 15;
+  const long long t = t0 + i;
+  KvGroup s{-1, 0, false, 0};
+  if (t < w.T) {
     const long long slot = w.slots[t];
-    bool ok = row < rows && slot >= 0;
-    const float *tab = nullptr;
-    if (ok && slot >= a.slots_total) {
-      set_device_error(HQ_ERR_DEVICE_INDEX);
-      ok = false;
+    if (slot >= a.slots_total) set_device_error(HQ_ERR_DEVICE_INDEX);
+    if (slot >= 0 && slot < a.slots_total) {
+      const long long pg = slot >> 31 ? slot / a.page : (long long)((uint32_t)slot / (uint32_t)a.page);
+      const int off = (int)(slot - pg * a.page);
+      s.unit = (long long)((size_t)pg * a.page_bytes + (size_t)(off >> 4) * kv_unit_bytes(FMT, D));
+      s.row = off & 15;
     }
-    if (ok && rope.rot) {
-      const int p = rope.pos[t];
-      if (p < 0 || p >= rope.P) {
+    if (rope && s.unit >= 0) {
+      const int p = rope->pos[t];
+      if (p < 0 || p >= rope->P) {
         set_device_error(HQ_ERR_DEVICE_INDEX);
-        ok = false;
-      } else {
-        tab = rope.table + (size_t)p * rope.rot;
+        s.unit = -1;
       }
     }
-    float fk[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, fv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (ok && on) {
-      const uint16_t *kr = w.k + t * w.ks + (size_t)h * D;
-      if (rope.rot) rope_octet(kr, o, rope.rot, rope.inter, tab, fk);
-      else unpack8(*reinterpret_cast<const uint4 *>(kr + 8 * o), fk);
-      unpack8(*reinterpret_cast<const uint4 *>(w.v + t * w.vs + (size_t)h * D + 8 * o), fv);
+  }
+  const int r0 = __shfl_sync(0xffffffffu, s.row, 0);
+  const long long u0 = __shfl_sync(0xffffffffu, s.unit, 0), u1 = __shfl_sync(0xffffffffu, s.unit, 15);
+  s.run = __all_sync(0xffffffffu, s.unit >= 0 && s.row == ((r0 + i) & 15) && s.unit == (r0 + i < 16 ? u0 : u1));
+  s.r0 = s.run ? r0 : 0;
+  return s;
+}
+
+// One of a lane's rows: the token of the call, and where it is held.
+struct KvRow {
+  int i, row;
+  long long unit;
+};
+__device__ __forceinline__ KvRow kv_row(const KvGroup &s, int r) {  // r: the lane's row in the layout
+  KvRow k;
+  k.i = (r - s.r0) & 15;
+  k.unit = __shfl_sync(0xffffffffu, s.unit, k.i);
+  k.row = __shfl_sync(0xffffffffu, s.row, k.i);
+  return k;
+}
+
+__device__ __forceinline__ float amax8(const float *f) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
+  return m;
+}
+// hq_quant_act's per-token recipe on a head's D channels
+__device__ __forceinline__ float e4m3_scale(float amax) { return (amax == 0.f) ? 1.f : __fdiv_rn(amax, 448.f); }
+// Correctly rounded quotients by one divisor, by Markstein's theorem ("Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990): with
+// y the correctly rounded 1 / d and q within one step of x / d, r = x - q d is
+// exact in an fma and q + r y, rounded, is the correctly rounded x / d, as
+// long as nothing over- or underflows.  y and the rest of 1 / d make a first
+// q that is off by little more than half a step.  Four instructions and the
+// sign (a zero keeps it) instead of a division each.  Rows whose divisor or
+// largest element is out of range divide.  (Dividends too small for an exact
+// r have quotients far under half of the smallest code.)
+struct Divisor {
+  float d, y, rest;
+  bool plain;
+};
+__device__ __forceinline__ Divisor divisor(float d, float amax) {
+  const float y = __frcp_rn(d);
+  return Divisor{d, y, __fmul_rn(__fmaf_rn(-d, y, 1.f), y), !(d > 1e-18f && d < 1e18f && amax < 1e18f)};
+}
+__device__ __forceinline__ float quotient(float x, const Divisor &v) {
+  if (v.plain) return __fdiv_rn(x, v.d);
+  const float q = __fmaf_rn(x, v.y, __fmul_rn(x, v.rest));
+  return copysignf(__fmaf_rn(__fmaf_rn(-q, v.d, x), v.y, q), x);
+}
+__device__ __forceinline__ uint2 e4m3_octet(const float *f, const Divisor &s) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = f32x2_to_e4m3x2(quotient(f[2 * i], s), quotient(f[2 * i + 1], s));
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+// hq_quant_act's NVFP4 recipe with a static tensor scale, on a block of 16
+__device__ __forceinline__ uint32_t nvfp4_scale(float amax, float g) {
+  return f32x2_to_e4m3x2(__fdiv_rn(__fdiv_rn(amax, 6.f), g), 0.f) & 0xFFu;
+}
+__device__ __forceinline__ uint32_t nvfp4_octet(const float *f, uint32_t sb, float g, float amax) {
+  const float d = __fmul_rn(e4m3_to_f32(sb), g);
+  if (d == 0.f) return 0;
+  const Divisor v = divisor(d, amax);
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w |= f32x2_to_e2m1x2(quotient(f[2 * i], v), quotient(f[2 * i + 1], v)) << (8 * i);
+  return w;
+}
+
+// Bound by HBM: WRITE_NOTE
+template <int FMT, int D, bool ROPE>
+__global__ void __launch_bounds__(KV_THREADS, D <= 128 ? 12 : 8)
+    kv_write_kernel(KvArgs a, KvRows w, RopeArgs rope, int kv_blocks) {
+  if (blockIdx.x >= kv_blocks) {  // these rotate the rope.H heads of q
+    rope_rows(rope, blockIdx.x - kv_blocks);
+    return;
+  }
+  constexpr int NB = D / 32, NQ = D / 64, CB = kv_code_bytes(FMT, D), SB = kv_scale_bytes(FMT, D), GS = kv_granule(FMT);
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const long long work = ((long long)w.T + 15) / 16 * a.H * 2, step = (long long)kv_blocks * (KV_THREADS / 32);
+  for (long long it = blockIdx.x * (KV_THREADS / 32) + (threadIdx.x >> 5); it < work; it += step) {
+    const bool is_v = it & 1;
+    const long long ih = it >> 1, grp = ih >> 31 ? ih / a.H : (long long)((uint32_t)ih / (uint32_t)a.H);
+    const int h = (int)(ih - grp * a.H);
+    const long long t0 = grp * 16;
+    const KvGroup s = kv_group<FMT, D>(a, w, ROPE ? &rope : nullptr, t0);
+    uint8_t *base = a.pages + (size_t)h * a.page_units * kv_unit_bytes(FMT, D);
+
+    if (!is_v) {
+      KvRow kr[2];
+      const uint16_t *x[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        kr[k] = kv_row(s, g + 8 * k);
+        x[k] = w.k + (t0 + kr[k].i) * w.ks + (size_t)h * D;
+      }
+      uint4 kx[2][NB];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          kx[k][b] = !ROPE && kr[k].unit >= 0 ? *reinterpret_cast<const uint4 *>(x[k] + 32 * b + 8 * t) : make_uint4(0, 0, 0, 0);
+      auto keys = [&](int k, float (&f)[NB][8]) {  // the lane's octets of key k as fp32
+        if constexpr (ROPE) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[b][i] = 0.f;
+          if (kr[k].unit >= 0)
+            rope_octets<NB>(x[k], t, rope.rot, rope.inter, rope.table + (size_t)rope.pos[t0 + kr[k].i] * rope.rot, f);
+        } else {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) unpack8(kx[k][b], f[b]);
+        }
+      };
+      const bool whole = s.run && kr[0].unit == kr[1].unit;
+      if constexpr (FMT == A_BF16) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if constexpr (ROPE) {
+            float f[NB][8];
+            keys(k, f);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) kx[k][b] = pack8(f[b]);
+          }
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            if (kr[k].unit >= 0)
+              *reinterpret_cast<uint4 *>(base + kr[k].unit + k_octet<GS>(4 * b + t, kr[k].row)) = kx[k][b];
+        }
+      } else if constexpr (FMT == A_FP8) {
+        uint2 c[2][NB];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float amax = 0.f, f[NB][8];
+          keys(k, f);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) amax = fmaxf(amax, amax8(f[b]));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          const Divisor sc = divisor(e4m3_scale(amax), amax);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) c[k][b] = e4m3_octet(f[b], sc);
+          if (t == 0 && kr[k].unit >= 0) reinterpret_cast<float *>(base + kr[k].unit + 2 * CB)[kr[k].row] = sc.d;
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          if (whole) {
+            *reinterpret_cast<uint4 *>(base + kr[0].unit + (b * 32 + lane) * 16) =
+                make_uint4(c[0][b].x, c[0][b].y, c[1][b].x, c[1][b].y);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              if (kr[k].unit >= 0)
+                *reinterpret_cast<uint2 *>(base + kr[k].unit + k_octet<GS>(4 * b + t, kr[k].row)) = c[k][b];
+          }
+        }
+      } else {
+        const float gl = a.glob[0];
+        uint32_t c[2][NB];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float f[NB][8];
+          keys(k, f);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            float amax = amax8(f[b]);
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            const uint32_t sb = nvfp4_scale(amax, gl);
+            c[k][b] = nvfp4_octet(f[b], sb, gl, amax);
+            if ((t & 1) == 0 && kr[k].unit >= 0)
+              base[kr[k].unit + 2 * CB + kr[k].row * (D / 16) + (t >> 1) * NB + b] = (uint8_t)sb;
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < NB; b += 2) {
+          if (whole) {
+            *reinterpret_cast<uint4 *>(base + kr[0].unit + (b * 16 + lane) * 16) =
+                make_uint4(c[0][b], c[1][b], c[0][b + 1], c[1][b + 1]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (kr[k & 1].unit >= 0)
+                *reinterpret_cast<uint32_t *>(base + kr[k & 1].unit + k_octet<GS>(4 * (b + (k >> 1)) + t, kr[k & 1].row)) =
+                    c[k & 1][b + (k >> 1)];
+          }
+        }
+      }
+      continue;
     }
-    int r = 0;
-    uint8_t *unit = ok ? kv_unit<FMT, D>(a, slot, h, r) : a.pages;
-    // the lanes of a row that is not stored still take part in the shuffles
-    if (__any_sync(0xffffffffu, ok)) {
-      kv_store<FMT, D, LPR>(unit, r, o, ok && on, false, fk, a.glob);
-      kv_store<FMT, D, LPR>(unit, r, o, ok && on, true, fv, a.glob);
+
+    KvRow vr[4];
+    uint4 vx[4][NQ];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      vr[k] = kv_row(s, 2 * t + (k & 1) + 8 * (k >> 1));
+      const uint16_t *x = w.v + (t0 + vr[k].i) * w.vs + (size_t)h * D + g * (D / 8);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+        vx[k][q] = vr[k].unit >= 0 ? *reinterpret_cast<const uint4 *>(x + 8 * q) : make_uint4(0, 0, 0, 0);
+    }
+    if constexpr (FMT == A_BF16) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+          if (vr[k].unit >= 0)
+            *reinterpret_cast<uint4 *>(base + vr[k].unit + CB + v_octet<GS, D>(g * NQ + q, vr[k].row)) = vx[k][q];
+    } else if constexpr (FMT == A_FP8) {
+      uint2 c[4][NQ];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float amax = 0.f, f[8];
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          unpack8(vx[k][q], f);
+          amax = fmaxf(amax, amax8(f));
+        }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const Divisor sc = divisor(e4m3_scale(amax), amax);
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          unpack8(vx[k][q], f);
+          c[k][q] = e4m3_octet(f, sc);
+        }
+        if (g == 0 && vr[k].unit >= 0) reinterpret_cast<float *>(base + vr[k].unit + 2 * CB + SB)[vr[k].row] = sc.d;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        const bool whole = s.run && vr[k].unit == vr[k + 1].unit;
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          if (whole) {
+            *reinterpret_cast<uint4 *>(base + vr[k].unit + CB + ((q * 2 + k / 2) * 32 + lane) * 16) =
+                make_uint4(c[k][q].x, c[k][q].y, c[k + 1][q].x, c[k + 1][q].y);
+          } else {
+#pragma unroll
+            for (int j = k; j < k + 2; ++j)
+              if (vr[j].unit >= 0)
+                *reinterpret_cast<uint2 *>(base + vr[j].unit + CB + v_octet<GS, D>(g * NQ + q, vr[j].row)) = c[j][q];
+          }
+        }
+      }
+    } else {
+      const float gl = a.glob[1];
+      uint32_t c[4][NQ];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float am[NQ];
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          float f[8];
+          unpack8(vx[k][q], f);
+          am[q] = amax8(f);
+        }
+        // a block is octets 2j and 2j + 1: neighbours in the lane, or the lane's last and the next one's first
+        const float over = __shfl_xor_sync(0xffffffffu, (g & 1) ? am[0] : am[NQ - 1], 4);
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          const int o = g * NQ + q, qq = q + ((o & 1) ? -1 : 1);  // the block's other octet
+          const float amax = fmaxf(am[q], qq >= 0 && qq < NQ ? am[(qq + NQ) % NQ] : over);
+          const uint32_t sb = nvfp4_scale(amax, gl);
+          float f[8];
+          unpack8(vx[k][q], f);
+          c[k][q] = nvfp4_octet(f, sb, gl, amax);
+          if ((o & 1) == 0 && vr[k].unit >= 0) base[vr[k].unit + 2 * CB + SB + (o >> 1) * 16 + vr[k].row] = (uint8_t)sb;
+        }
+      }
+      const bool whole = s.run && vr[0].unit == vr[1].unit && vr[0].unit == vr[2].unit && vr[0].unit == vr[3].unit;
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        if (whole) {
+          *reinterpret_cast<uint4 *>(base + vr[0].unit + CB + (q * 32 + lane) * 16) =
+              make_uint4(c[0][q], c[1][q], c[2][q], c[3][q]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (vr[k].unit >= 0)
+              *reinterpret_cast<uint32_t *>(base + vr[k].unit + CB + v_octet<GS, D>(g * NQ + q, vr[k].row)) = c[k][q];
+        }
+      }
     }
   }
 }
 
+// Two codes as fp16 (exact), and an octet's values as bf16 pairs: the product
+// with the scale(s) in fp32, then one rounding.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)c));
+  return r;
+}
+template <int I>
+__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t w) {  // byte I of w
+  uint32_t r;
+  if constexpr (I == 0) asm("{.reg .b8 a,b,c,d; mov.b32 {a,b,c,d}, %1; cvt.rn.f16x2.e2m1x2 %0, a;}" : "=r"(r) : "r"(w));
+  if constexpr (I == 1) asm("{.reg .b8 a,b,c,d; mov.b32 {a,b,c,d}, %1; cvt.rn.f16x2.e2m1x2 %0, b;}" : "=r"(r) : "r"(w));
+  if constexpr (I == 2) asm("{.reg .b8 a,b,c,d; mov.b32 {a,b,c,d}, %1; cvt.rn.f16x2.e2m1x2 %0, c;}" : "=r"(r) : "r"(w));
+  if constexpr (I == 3) asm("{.reg .b8 a,b,c,d; mov.b32 {a,b,c,d}, %1; cvt.rn.f16x2.e2m1x2 %0, d;}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h, float s) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+  return bf16x2(__fmul_rn(f.x, s), __fmul_rn(f.y, s));
+}
+__device__ __forceinline__ uint4 e4m3_values(uint32_t lo, uint32_t hi, float s) {
+  return make_uint4(scaled_bf16x2(e4m3x2_to_f16x2(lo), s), scaled_bf16x2(e4m3x2_to_f16x2(lo >> 16), s),
+                    scaled_bf16x2(e4m3x2_to_f16x2(hi), s), scaled_bf16x2(e4m3x2_to_f16x2(hi >> 16), s));
+}
+__device__ __forceinline__ uint4 nvfp4_values(uint32_t w, uint32_t sb, float g) {
+  const uint32_t s = __byte_perm(e4m3x2_to_f16x2(sb), 0, 0x1010);  // code times block scale is exact in fp16
+  return make_uint4(scaled_bf16x2(hmul2(e2m1x2_to_f16x2<0>(w), s), g), scaled_bf16x2(hmul2(e2m1x2_to_f16x2<1>(w), s), g),
+                    scaled_bf16x2(hmul2(e2m1x2_to_f16x2<2>(w), s), g), scaled_bf16x2(hmul2(e2m1x2_to_f16x2<3>(w), s), g));
+}
+
+// Bound by HBM: READ_NOTE
 template <int FMT, int D>
-__global__ void __launch_bounds__(256) kv_read_kernel(KvArgs a, KvRows w) {
-  constexpr int LPR = kv_lpr<D>();
-  const int o = threadIdx.x % LPR;
-  if (o >= D / 8) return;
-  const size_t rows = (size_t)w.T * a.H, step = (size_t)gridDim.x * (256 / LPR);
-  for (size_t row = blockIdx.x * (size_t)(256 / LPR) + threadIdx.x / LPR; row < rows; row += step) {
-    const size_t t = row / a.H;
-    const int h = (int)(row % a.H);
-    const long long slot = w.slots[t];
-    if (slot < 0) continue;
-    if (slot >= a.slots_total) {
-      set_device_error(HQ_ERR_DEVICE_INDEX);
-      continue;
+__global__ void __launch_bounds__(KV_THREADS, 12) kv_read_kernel(KvArgs a, KvRows w) {
+  constexpr int NB = D / 32, NQ = D / 64, CB = kv_code_bytes(FMT, D), SB = kv_scale_bytes(FMT, D), GS = kv_granule(FMT);
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const long long work = ((long long)w.T + 15) / 16 * a.H * 2, step = (long long)gridDim.x * (KV_THREADS / 32);
+  for (long long it = blockIdx.x * (KV_THREADS / 32) + (threadIdx.x >> 5); it < work; it += step) {
+    const bool is_v = it & 1;
+    if (!(is_v ? w.v_out : w.k_out)) continue;
+    const long long ih = it >> 1, grp = ih >> 31 ? ih / a.H : (long long)((uint32_t)ih / (uint32_t)a.H);
+    const int h = (int)(ih - grp * a.H);
+    const long long t0 = grp * 16;
+    const KvGroup s = kv_group<FMT, D>(a, w, nullptr, t0);
+    const uint8_t *base = a.pages + (size_t)h * a.page_units * kv_unit_bytes(FMT, D);
+    // granule n of vector i: the octets of the lane's rows, whole or one by one
+    if (!is_v) {
+      KvRow kr[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) kr[k] = kv_row(s, g + 8 * k);
+      const bool whole = s.run && kr[0].unit == kr[1].unit;
+      constexpr int NV = NB * 2 * GS / 16;  // vectors
+      uint4 x[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (whole) {
+          x[i] = *reinterpret_cast<const uint4 *>(base + kr[0].unit + (i * 32 + lane) * 16);
+        } else {
+          uint32_t *p = reinterpret_cast<uint32_t *>(&x[i]);
+#pragma unroll
+          for (int n = 0; n < 16 / GS; ++n) {
+            const int gi = i * (16 / GS) + n, k = gi & 1;
+            if (kr[k].unit < 0) continue;
+            const uint8_t *from = base + kr[k].unit + k_octet<GS>(4 * (gi >> 1) + t, kr[k].row);
+            if constexpr (GS == 16) x[i] = *reinterpret_cast<const uint4 *>(from);
+            if constexpr (GS == 8) {
+              const uint2 y = *reinterpret_cast<const uint2 *>(from);
+              p[2 * n] = y.x;
+              p[2 * n + 1] = y.y;
+            }
+            if constexpr (GS == 4) p[n] = *reinterpret_cast<const uint32_t *>(from);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (kr[k].unit < 0) continue;
+        uint16_t *to = w.k_out + (t0 + kr[k].i) * w.ks + (size_t)h * D + 8 * t;
+        const uint8_t *sc = base + kr[k].unit + 2 * CB;
+        float fs = 1.f;
+        if constexpr (FMT == A_FP8) fs = reinterpret_cast<const float *>(sc)[kr[k].row];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          uint4 v;
+          if constexpr (FMT == A_BF16) v = x[2 * b + k];
+          if constexpr (FMT == A_FP8) v = k ? e4m3_values(x[b].z, x[b].w, fs) : e4m3_values(x[b].x, x[b].y, fs);
+          if constexpr (FMT == A_NVFP4) {
+            const uint4 y = x[b >> 1];
+            const uint32_t c = (b & 1) ? (k ? y.w : y.z) : (k ? y.y : y.x);
+            v = nvfp4_values(c, sc[kr[k].row * (D / 16) + (t >> 1) * NB + b], a.glob[0]);
+          }
+          *reinterpret_cast<uint4 *>(to + 32 * b) = v;
+        }
+      }
     }
-    int r;
-    const uint8_t *unit = kv_unit<FMT, D>(a, slot, h, r);
-    float f[8];
-    if (w.k_out) {
-      kv_load<FMT, D>(unit, r, o, false, a.glob, f);
-      *reinterpret_cast<uint4 *>(w.k_out + t * w.ks + (size_t)h * D + 8 * o) = pack8(f);
-    }
-    if (w.v_out) {
-      kv_load<FMT, D>(unit, r, o, true, a.glob, f);
-      *reinterpret_cast<uint4 *>(w.v_out + t * w.vs + (size_t)h * D + 8 * o) = pack8(f);
+    if (is_v) {
+      KvRow vr[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) vr[k] = kv_row(s, 2 * t + (k & 1) + 8 * (k >> 1));
+      bool same[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)  // with the other octets of its vector
+        same[k] = s.run && (FMT == A_FP8 ? vr[k].unit == vr[k ^ 1].unit
+                                         : vr[0].unit == vr[1].unit && vr[0].unit == vr[2].unit && vr[0].unit == vr[3].unit);
+      constexpr int NV = NQ * 4 * GS / 16;
+      uint4 x[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        x[i] = make_uint4(0, 0, 0, 0);
+        const int k0 = i * (16 / GS) & 3;  // the first octet's row
+        if (GS < 16 && same[k0]) {
+          x[i] = *reinterpret_cast<const uint4 *>(base + vr[k0].unit + CB + (i * 32 + lane) * 16);
+        } else {
+          uint32_t *p = reinterpret_cast<uint32_t *>(&x[i]);
+#pragma unroll
+          for (int n = 0; n < 16 / GS; ++n) {
+            const int gi = i * (16 / GS) + n, k = gi & 3;
+            if (vr[k].unit < 0) continue;
+            const uint8_t *from = base + vr[k].unit + CB + v_octet<GS, D>(g * NQ + (gi >> 2), vr[k].row);
+            if constexpr (GS == 16) x[i] = *reinterpret_cast<const uint4 *>(from);
+            if constexpr (GS == 8) {
+              const uint2 y = *reinterpret_cast<const uint2 *>(from);
+              p[2 * n] = y.x;
+              p[2 * n + 1] = y.y;
+            }
+            if constexpr (GS == 4) p[n] = *reinterpret_cast<const uint32_t *>(from);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (vr[k].unit < 0) continue;
+        uint16_t *to = w.v_out + (t0 + vr[k].i) * w.vs + (size_t)h * D + g * (D / 8);
+        const uint8_t *sc = base + vr[k].unit + 2 * CB + SB;
+        float fs = 1.f;
+        if constexpr (FMT == A_FP8) fs = reinterpret_cast<const float *>(sc)[vr[k].row];
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          uint4 v;
+          if constexpr (FMT == A_BF16) v = x[4 * q + k];
+          if constexpr (FMT == A_FP8) {
+            const uint4 y = x[2 * q + (k >> 1)];
+            v = (k & 1) ? e4m3_values(y.z, y.w, fs) : e4m3_values(y.x, y.y, fs);
+          }
+          if constexpr (FMT == A_NVFP4) {
+            const uint32_t c = k == 0 ? x[q].x : k == 1 ? x[q].y : k == 2 ? x[q].z : x[q].w;
+            v = nvfp4_values(c, sc[((g * NQ + q) >> 1) * 16 + vr[k].row], a.glob[1]);
+          }
+          *reinterpret_cast<uint4 *>(to + 8 * q) = v;
+        }
+      }
     }
   }
 }
@@ -474,18 +934,27 @@ static hq_status kv_dispatch(int fmt, int D, F &&f) {
   return HQ_ERR_UNSUPPORTED;
 }
 
+static int kv_blocks(const KvArgs &a, const KvRows &w) {
+  const long long work = (((long long)w.T + 15) / 16 * a.H * 2 + KV_THREADS / 32 - 1) / (KV_THREADS / 32);
+  return (int)(work < 148 * 12 ? work : 148 * 12);
+}
+
 hq_status launch_kv_write(int fmt, int D, const KvArgs &a, const KvRows &w, const RopeArgs &rope, cudaStream_t st) {
   return kv_dispatch(fmt, D, [&](auto F, auto DD) {
-    const int kb = quant_grid((size_t)w.T * a.H * kv_lpr<DD>(), 256);
-    const int qb = rope.H ? quant_grid((size_t)rope.T * rope.H * rope_chunks(rope.D, rope.rot), 256) : 0;
-    kv_write_kernel<F, DD><<<kb + qb, 256, 0, st>>>(a, w, rope, kb);
+    const int kb = kv_blocks(a, w);
+    if (rope.rot) {
+      const int qb = rope.H ? (int)rope_blocks(rope) : 0;
+      kv_write_kernel<F, DD, true><<<kb + qb, KV_THREADS, 0, st>>>(a, w, rope, kb);
+    } else {
+      kv_write_kernel<F, DD, false><<<kb, KV_THREADS, 0, st>>>(a, w, rope, kb);
+    }
     return check_launch();
   });
 }
 
 hq_status launch_kv_read(int fmt, int D, const KvArgs &a, const KvRows &w, cudaStream_t st) {
   return kv_dispatch(fmt, D, [&](auto F, auto DD) {
-    kv_read_kernel<F, DD><<<quant_grid((size_t)w.T * a.H * kv_lpr<DD>(), 256), 256, 0, st>>>(a, w);
+    kv_read_kernel<F, DD><<<kv_blocks(a, w), KV_THREADS, 0, st>>>(a, w);
     return check_launch();
   });
 }

@@ -218,6 +218,59 @@ def test_write_read(dtype, H, D, page, T, order):
         assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("dtype", ["e4m3", "nvfp4"])
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+def test_write_read_rows_of_any_size(dtype, D):
+    """Rows from the smallest to the largest bf16 numbers, zeros of both signs, and quotients that are ties: the codes
+    are the recipe's (fp32 division) bit for bit."""
+    exps = [-133, -126, -100, -84, -61, -59, -40, -9, 0, 13, 59, 61, 84, 100, 127]
+    T = len(exps) + 17
+    c = Cache(dtype, 1, D, 16, 3)
+    k, v = normal((T, 1, D), 25), normal((T, 1, D), 26)
+    for i, e in enumerate(exps):
+        for x in (k, v):
+            x[i] = (x[i].double() / 4 * 2.0**e).to(torch.bfloat16).clamp(-3.3e38, 3.3e38)
+    k[-1, 0, ::3] = -0.0
+    v[-2] = -0.0
+    grid = torch.tensor([448, 17, -17, 19, -19, 0.25, 1.0625, -1.1875, 2.5, -3.5, 5, 0.75]).repeat(D // 12 + 1)[:D]
+    k[-3, 0], v[-3, 0] = grid.to(torch.bfloat16), (grid / 64).to(torch.bfloat16)
+    slots = torch.arange(T) + 5  # a run through units that starts inside one
+    c.write(k, v, slots)
+    rk, rv = c.read(slots)
+    for got, x, g in ((rk, k, GLOB[0]), (rv, v, GLOB[1])):
+        want, _ = expected_read(x, dtype, g)
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+    # a row with infinities spoils no other
+    k[3, 0, 5] = math.inf
+    c.write(k, v, slots)
+    again, _ = c.read(slots)
+    keep = [i for i in range(T) if i != 3]
+    assert torch.equal(again[keep], rk[keep])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "nvfp4"])
+@pytest.mark.parametrize("first", [0, 1, 7, 8, 9, 15])
+@pytest.mark.parametrize("page", [16, 48])
+def test_runs_that_start_anywhere(dtype, first, page):
+    """A prompt's slots: any first row, page ends inside a group of 16, a gap, and a tail."""
+    T, H, D = 70, 2, 128
+    perm = torch.randperm(8, generator=gen(27))
+    at = torch.arange(T) + first
+    slots = perm[at // page] * page + at % page
+    slots[40] = -1
+    c = Cache(dtype, H, D, page, 8, fill=0x3C)
+    k, v = normal((T, H, D), 28), normal((T, H, D), 29)
+    c.write(k, v, slots)
+    rk, rv = c.read(slots, fill=2.0)
+    for got, x, g in ((rk, k, GLOB[0]), (rv, v, GLOB[1])):
+        want, _ = expected_read(x, dtype, g)
+        want[40] = 2.0
+        assert torch.equal(got, want)
+    back = torch.arange(T - 1, -1, -1)  # the same slots one by one, in another order
+    bk, bv = c.read(slots[back], fill=2.0)
+    assert torch.equal(bk[back], rk) and torch.equal(bv[back], rv)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3", "nvfp4"])
 @pytest.mark.parametrize("D", [64, 128, 192, 256])
 def test_only_the_named_slots_change(dtype, D):
