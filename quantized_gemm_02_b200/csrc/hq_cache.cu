@@ -298,6 +298,14 @@ RopeArgs rope_args(int T, int H, int D, const hq_rope_desc *r, int P, const void
                   ot, oh, fast_div(nc), fast_div(per_token), fast_div(split.parts), split.tokens};
 }
 
+// The same rotation for blocks of another width.
+inline RopeArgs rope_resplit(RopeArgs a, int threads) {
+  const RopeSplit split = rope_split(a.T, a.per_token.d, threads);
+  a.parts = fast_div(split.parts);
+  a.tokens = split.tokens;
+  return a;
+}
+
 hq_status launch_rope(const RopeArgs &a, cudaStream_t st) {
   rope_kernel<<<(unsigned)rope_blocks(a), ROPE_THREADS, 0, st>>>(a);
   return check_launch();
@@ -486,29 +494,61 @@ __device__ __forceinline__ Divisor divisor(float d, float amax) {
   const float y = __frcp_rn(d);
   return Divisor{d, y, __fmul_rn(__fmaf_rn(-d, y, 1.f), y), !(d > 1e-18f && d < 1e18f && amax < 1e18f)};
 }
-__device__ __forceinline__ float quotient(float x, const Divisor &v) {
-  if (v.plain) return __fdiv_rn(x, v.d);
+__device__ __forceinline__ float quotient(float x, const Divisor &v) {  // not v.plain
   const float q = __fmaf_rn(x, v.y, __fmul_rn(x, v.rest));
   return copysignf(__fmaf_rn(__fmaf_rn(-q, v.d, x), v.y, q), x);
 }
-__device__ __forceinline__ uint2 e4m3_octet(const float *f, const Divisor &s) {
-  uint32_t w[4];
+// Four codes a word.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{.reg .b16 l,h; cvt.rn.satfinite.e4m3x2.f32 l, %2, %1; cvt.rn.satfinite.e4m3x2.f32 h, %4, %3; mov.b32 %0, {l,h};}"
+      : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+__device__ __forceinline__ uint32_t e2m1x8(const float *f) {
+  uint32_t r;
+  asm("{.reg .b8 a,b,c,d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1; cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5; cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a,b,c,d};}"
+      : "=r"(r) : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+  return r;
+}
+struct Octet {
+  float f[8];
+};
+__device__ __noinline__ Octet octet_divided(Octet x, float d) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = f32x2_to_e4m3x2(quotient(f[2 * i], s), quotient(f[2 * i + 1], s));
-  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+  for (int i = 0; i < 8; ++i) x.f[i] = __fdiv_rn(x.f[i], d);
+  return x;
+}
+__device__ __forceinline__ Octet octet_quotients(const float *f, const Divisor &v) {
+  Octet x;
+  if (v.plain) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x.f[i] = f[i];
+    return octet_divided(x, v.d);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x.f[i] = quotient(f[i], v);
+  return x;
+}
+__device__ __forceinline__ uint2 e4m3_octet(const float *f, const Divisor &s) {
+  const Octet x = octet_quotients(f, s);
+  return make_uint2(e4m3x4(x.f[0], x.f[1], x.f[2], x.f[3]), e4m3x4(x.f[4], x.f[5], x.f[6], x.f[7]));
 }
 // hq_quant_act's NVFP4 recipe with a static tensor scale, on a block of 16
-__device__ __forceinline__ uint32_t nvfp4_scale(float amax, float g) {
-  return f32x2_to_e4m3x2(__fdiv_rn(__fdiv_rn(amax, 6.f), g), 0.f) & 0xFFu;
+__device__ __noinline__ float nvfp4_scale_divided(float amax, float g) { return __fdiv_rn(__fdiv_rn(amax, 6.f), g); }
+__device__ __forceinline__ uint32_t nvfp4_scale(float amax, const Divisor &g) {
+  const Divisor six = divisor(6.f, 0.f);
+  const float s = g.plain || !(amax < 1e18f) ? nvfp4_scale_divided(amax, g.d) : quotient(quotient(amax, six), g);
+  return f32x2_to_e4m3x2(s, 0.f) & 0xFFu;
 }
 __device__ __forceinline__ uint32_t nvfp4_octet(const float *f, uint32_t sb, float g, float amax) {
   const float d = __fmul_rn(e4m3_to_f32(sb), g);
   if (d == 0.f) return 0;
-  const Divisor v = divisor(d, amax);
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w |= f32x2_to_e2m1x2(quotient(f[2 * i], v), quotient(f[2 * i + 1], v)) << (8 * i);
-  return w;
+  const Octet x = octet_quotients(f, divisor(d, amax));
+  return e2m1x8(x.f);
 }
 
 // Bound by HBM: WRITE_NOTE
@@ -601,6 +641,7 @@ __global__ void __launch_bounds__(KV_THREADS, D <= 128 ? 12 : 8)
         }
       } else {
         const float gl = a.glob[0];
+        const Divisor gd = divisor(gl, 0.f);
         uint32_t c[2][NB];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -610,7 +651,7 @@ __global__ void __launch_bounds__(KV_THREADS, D <= 128 ? 12 : 8)
           for (int b = 0; b < NB; ++b) {
             float amax = amax8(f[b]);
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            const uint32_t sb = nvfp4_scale(amax, gl);
+            const uint32_t sb = nvfp4_scale(amax, gd);
             c[k][b] = nvfp4_octet(f[b], sb, gl, amax);
             if ((t & 1) == 0 && kr[k].unit >= 0)
               base[kr[k].unit + 2 * CB + kr[k].row * (D / 16) + (t >> 1) * NB + b] = (uint8_t)sb;
@@ -688,6 +729,7 @@ __global__ void __launch_bounds__(KV_THREADS, D <= 128 ? 12 : 8)
       }
     } else {
       const float gl = a.glob[1];
+      const Divisor gd = divisor(gl, 0.f);
       uint32_t c[4][NQ];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -704,7 +746,7 @@ __global__ void __launch_bounds__(KV_THREADS, D <= 128 ? 12 : 8)
         for (int q = 0; q < NQ; ++q) {
           const int o = g * NQ + q, qq = q + ((o & 1) ? -1 : 1);  // the block's other octet
           const float amax = fmaxf(am[q], qq >= 0 && qq < NQ ? am[(qq + NQ) % NQ] : over);
-          const uint32_t sb = nvfp4_scale(amax, gl);
+          const uint32_t sb = nvfp4_scale(amax, gd);
           float f[8];
           unpack8(vx[k][q], f);
           c[k][q] = nvfp4_octet(f, sb, gl, amax);
@@ -943,8 +985,16 @@ hq_status launch_kv_write(int fmt, int D, const KvArgs &a, const KvRows &w, cons
   return kv_dispatch(fmt, D, [&](auto F, auto DD) {
     const int kb = kv_blocks(a, w);
     if (rope.rot) {
-      const int qb = rope.H ? (int)rope_blocks(rope) : 0;
-      kv_write_kernel<F, DD, true><<<kb + qb, KV_THREADS, 0, st>>>(a, w, rope, kb);
+      // A step's q is rotated by further blocks of the launch; a prompt's by
+      // the rotation's own kernel, whose blocks are four times as many to an SM
+      // (8191 x 16 heads x 256 beside the write: FUSED us against SPLIT).
+      const long long qb = rope.H ? rope_blocks(rope) : 0;
+      const bool split = qb > 148 * 4;
+      kv_write_kernel<F, DD, true><<<kb + (split ? 0 : (int)qb), KV_THREADS, 0, st>>>(a, w, rope, kb);
+      if (split) {
+        const hq_status s = check_launch();
+        return s != HQ_OK ? s : launch_rope(rope_resplit(rope, ROPE_THREADS), st);
+      }
     } else {
       kv_write_kernel<F, DD, false><<<kb, KV_THREADS, 0, st>>>(a, w, rope, kb);
     }
