@@ -137,7 +137,8 @@ __device__ __forceinline__ void load8(const float *p, float *f) {
 // Work of a head: chunks of 8 pairs, then chunks of 16 unrotated channels (the
 // last may have 8 or, where pairs straddle 16-byte pieces, any number).  A
 // chunk holds both channels of its pairs, so x and out may be the same.
-__host__ __device__ inline int rope_chunks(int D, int rot) { return (rot / 2 + 7) / 8 + (D - rot + 15) / 16; }
+inline int rope_pairs(int rot) { return (rot / 2 + 7) / 8; }
+inline int rope_rest(int D, int rot) { return (D - rot + 15) / 16; }
 
 // rot_dim a multiple of 16: a chunk is two 16-byte pieces (the second may be
 // missing), loaded before anything that depends on the position.
@@ -145,7 +146,7 @@ struct RopePiece {
   const uint16_t *x;  // the head's row, or null: no chunk
   uint16_t *out;
   long long t;
-  int c;
+  int c, p;  // chunk, position
   uint4 a, b;
 };
 __device__ __forceinline__ void rope_where(const RopePiece &r, int D, int rot, int inter, int &i0, int &i1, bool &pair) {
@@ -165,8 +166,8 @@ __device__ __forceinline__ void rope_piece(const RopePiece &r, int D, int rot, i
   rope_where(r, D, rot, inter, i0, i1, pair);
   if (!pair) {
     if (r.x == r.out) return;
-    *reinterpret_cast<uint4 *>(r.out + i0) = r.a;
-    if (i1 >= 0) *reinterpret_cast<uint4 *>(r.out + i1) = r.b;
+    __stcs(reinterpret_cast<uint4 *>(r.out + i0), r.a);
+    if (i1 >= 0) __stcs(reinterpret_cast<uint4 *>(r.out + i1), r.b);
     return;
   }
   float a[8], b[8], co[8], si[8];
@@ -184,8 +185,8 @@ __device__ __forceinline__ void rope_piece(const RopePiece &r, int D, int rot, i
 #pragma unroll
     for (int j = 0; j < 8; ++j) rope_pair(a[j], b[j], co[j], si[j], a[j], b[j]);
   }
-  *reinterpret_cast<uint4 *>(r.out + i0) = pack8(a);
-  *reinterpret_cast<uint4 *>(r.out + i1) = pack8(b);
+  __stcs(reinterpret_cast<uint4 *>(r.out + i0), pack8(a));
+  __stcs(reinterpret_cast<uint4 *>(r.out + i1), pack8(b));
 }
 
 // Other widths, channel by channel.
@@ -226,14 +227,14 @@ struct RopeArgs {
   const float *table;
   uint16_t *out;
   long long ot, oh;
-  FastDiv chunks, per_token;  // chunks of a head and of a token
+  FastDiv pairs, rest, per_token;  // chunks with and without pairs of a head, chunks of a token
   FastDiv parts;              // blocks of a token
   int tokens;                 // tokens of a block
 };
 
 // A block has up to ROPE_EACH chunks a thread: several whole tokens, or one of
 // `parts` parts of a token.
-constexpr int ROPE_EACH = 2;
+constexpr int ROPE_EACH = 1;
 struct RopeSplit {
   int tokens, parts;
 };
@@ -260,9 +261,12 @@ __device__ __forceinline__ void rope_rows(const RopeArgs &a, uint32_t block) {
     const uint32_t i = i0 + u * blockDim.x;
     r[u].x = nullptr;
     if (i >= n) continue;
-    const uint32_t tt = div_by(i, a.per_token), in = i - tt * a.per_token.d, h = div_by(in, a.chunks);
-    r[u].c = in - h * a.chunks.d;
+    // a token's pairs come first, head by head, then the rest, so that warps rarely do both
+    const uint32_t tt = div_by(i, a.per_token), in = i - tt * a.per_token.d, np = a.H * a.pairs.d;
+    const uint32_t j = in < np ? in : in - np, h = div_by(j, in < np ? a.pairs : a.rest);
+    r[u].c = in < np ? j - h * a.pairs.d : a.pairs.d + j - h * a.rest.d;
     r[u].t = t0 + tt;
+    r[u].p = a.pos[r[u].t];
     r[u].x = a.x + r[u].t * a.xt + h * a.xh;
     r[u].out = a.out + r[u].t * a.ot + h * a.oh;
     if (!fast) continue;
@@ -270,32 +274,31 @@ __device__ __forceinline__ void rope_rows(const RopeArgs &a, uint32_t block) {
     bool pair;
     rope_where(r[u], a.D, a.rot, a.inter, p0, p1, pair);
     if (!pair && r[u].x == r[u].out) continue;
-    r[u].a = *reinterpret_cast<const uint4 *>(r[u].x + p0);
-    if (p1 >= 0) r[u].b = *reinterpret_cast<const uint4 *>(r[u].x + p1);
+    r[u].a = __ldcs(reinterpret_cast<const uint4 *>(r[u].x + p0));
+    if (p1 >= 0) r[u].b = __ldcs(reinterpret_cast<const uint4 *>(r[u].x + p1));
   }
 #pragma unroll
   for (int u = 0; u < ROPE_EACH; ++u) {
     if (!r[u].x) continue;
-    const int p = a.pos[r[u].t];
-    if (p < 0 || p >= a.P) {
+    if (r[u].p < 0 || r[u].p >= a.P) {
       set_device_error(HQ_ERR_DEVICE_INDEX);
       continue;
     }
-    const float *tab = a.table + (size_t)p * a.rot;
+    const float *tab = a.table + (size_t)r[u].p * a.rot;
     if (fast) rope_piece(r[u], a.D, a.rot, a.inter, tab);
     else rope_slow(r[u].c, a.D, a.rot, a.inter, r[u].x, tab, r[u].out);
   }
 }
 
-constexpr int ROPE_THREADS = 256;
-__global__ void __launch_bounds__(ROPE_THREADS, 4) rope_kernel(RopeArgs a) { rope_rows(a, blockIdx.x); }
+constexpr int ROPE_THREADS = 128;
+__global__ void __launch_bounds__(ROPE_THREADS, 12) rope_kernel(RopeArgs a) { rope_rows(a, blockIdx.x); }
 
 RopeArgs rope_args(int T, int H, int D, const hq_rope_desc *r, int P, const void *x, int64_t xt, int64_t xh,
                    const int32_t *pos, const float *table, void *out, int64_t ot, int64_t oh, int threads) {
-  const int nc = rope_chunks(D, r->rot_dim), per_token = nc * (H > 0 ? H : 1);
+  const int pairs = rope_pairs(r->rot_dim), rest = rope_rest(D, r->rot_dim), per_token = (pairs + rest) * (H > 0 ? H : 1);
   const RopeSplit split = rope_split(T, per_token, threads);
   return RopeArgs{T, H, D, r->rot_dim, r->interleaved, P, (const uint16_t *)x, xt, xh, pos, table, (uint16_t *)out,
-                  ot, oh, fast_div(nc), fast_div(per_token), fast_div(split.parts), split.tokens};
+                  ot, oh, fast_div(pairs), fast_div(rest > 0 ? rest : 1), fast_div(per_token), fast_div(split.parts), split.tokens};
 }
 
 // The same rotation for blocks of another width.
@@ -358,45 +361,35 @@ __device__ __noinline__ void rope_octet_slow(const uint16_t *x, int o, int rot, 
   }
 }
 
-// A lane's octets 4 b + t of a row, rotated in fp32.
-template <int NB>
-__device__ __forceinline__ void rope_octets(const uint16_t *x, int t, int rot, int inter, const float *tab, float (&f)[NB][8]) {
-  const int half = rot / 2;
+__device__ __forceinline__ void rope_octet(const uint16_t *x, int o, int rot, int inter, const float *tab, float *f) {
+  const int half = rot / 2, ch = 8 * o;
   if (rot & 15) {
+    float tmp[8];
+    rope_octet_slow(x, o, rot, inter, tab, tmp);
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      float tmp[8];
-      rope_octet_slow(x, 4 * b + t, rot, inter, tab, tmp);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[b][i] = tmp[i];
-    }
+    for (int i = 0; i < 8; ++i) f[i] = tmp[i];
     return;
   }
+  unpack8(*reinterpret_cast<const uint4 *>(x + ch), f);
+  if (ch >= rot) return;
+  if (inter) {  // the pairs are within the octet
+    const float4 co = *reinterpret_cast<const float4 *>(tab + ch / 2), si = *reinterpret_cast<const float4 *>(tab + half + ch / 2);
+    rope_pair(f[0], f[1], co.x, si.x, f[0], f[1]);
+    rope_pair(f[2], f[3], co.y, si.y, f[2], f[3]);
+    rope_pair(f[4], f[5], co.z, si.z, f[4], f[5]);
+    rope_pair(f[6], f[7], co.w, si.w, f[6], f[7]);
+  } else {
+    const bool second = ch >= half;
+    const int j = second ? ch - half : ch;
+    float p[8], co[8], si[8];
+    unpack8(*reinterpret_cast<const uint4 *>(x + (second ? j : ch + half)), p);
+    load8(tab + j, co);
+    load8(tab + half + j, si);
 #pragma unroll
-  for (int b = 0; b < NB; ++b) unpack8(*reinterpret_cast<const uint4 *>(x + 32 * b + 8 * t), f[b]);
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const int ch = 32 * b + 8 * t;
-    if (ch >= rot) continue;
-    if (inter) {  // the pairs are within the octet
-      const float4 co = *reinterpret_cast<const float4 *>(tab + ch / 2), si = *reinterpret_cast<const float4 *>(tab + half + ch / 2);
-      rope_pair(f[b][0], f[b][1], co.x, si.x, f[b][0], f[b][1]);
-      rope_pair(f[b][2], f[b][3], co.y, si.y, f[b][2], f[b][3]);
-      rope_pair(f[b][4], f[b][5], co.z, si.z, f[b][4], f[b][5]);
-      rope_pair(f[b][6], f[b][7], co.w, si.w, f[b][6], f[b][7]);
-    } else {
-      const bool second = ch >= half;
-      const int j = second ? ch - half : ch;
-      float p[8], co[8], si[8];
-      unpack8(*reinterpret_cast<const uint4 *>(x + (second ? j : ch + half)), p);
-      load8(tab + j, co);
-      load8(tab + half + j, si);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        // a c - b s for the first of a pair, b c + a s for the second
-        const float u = __fmul_rn(f[b][i], co[i]), v = __fmul_rn(p[i], si[i]);
-        f[b][i] = second ? __fadd_rn(u, v) : __fsub_rn(u, v);
-      }
+    for (int i = 0; i < 8; ++i) {
+      // a c - b s for the first of a pair, b c + a s for the second
+      const float u = __fmul_rn(f[i], co[i]), v = __fmul_rn(p[i], si[i]);
+      f[i] = second ? __fadd_rn(u, v) : __fsub_rn(u, v);
     }
   }
 }
@@ -551,9 +544,13 @@ __device__ __forceinline__ uint32_t nvfp4_octet(const float *f, uint32_t sb, flo
   return e2m1x8(x.f);
 }
 
+// Warps that share the octets of a group and head: 64 channels each, but for
+// E4M3, whose scale needs a whole row.
+__host__ __device__ constexpr int kv_parts(int fmt, int D) { return fmt == A_FP8 ? 1 : D / 64; }
+
 // Bound by HBM: WRITE_NOTE
 template <int FMT, int D, bool ROPE>
-__global__ void __launch_bounds__(KV_THREADS, D <= 128 ? 12 : 8)
+__global__ void __launch_bounds__(KV_THREADS, FMT == A_FP8 && ROPE ? 8 : 12)
     kv_write_kernel(KvArgs a, KvRows w, RopeArgs rope, int kv_blocks) {
   if (blockIdx.x >= kv_blocks) {  // these rotate the rope.H heads of q
     rope_rows(rope, blockIdx.x - kv_blocks);
@@ -561,10 +558,12 @@ __global__ void __launch_bounds__(KV_THREADS, D <= 128 ? 12 : 8)
   }
   constexpr int NB = D / 32, NQ = D / 64, CB = kv_code_bytes(FMT, D), SB = kv_scale_bytes(FMT, D), GS = kv_granule(FMT);
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const long long work = ((long long)w.T + 15) / 16 * a.H * 2, step = (long long)kv_blocks * (KV_THREADS / 32);
+  constexpr int PARTS = kv_parts(FMT, D);
+  const long long work = ((long long)w.T + 15) / 16 * a.H * 2 * PARTS, step = (long long)kv_blocks * (KV_THREADS / 32);
   for (long long it = blockIdx.x * (KV_THREADS / 32) + (threadIdx.x >> 5); it < work; it += step) {
-    const bool is_v = it & 1;
-    const long long ih = it >> 1, grp = ih >> 31 ? ih / a.H : (long long)((uint32_t)ih / (uint32_t)a.H);
+    const int part = (int)(it % PARTS);
+    const bool is_v = it / PARTS & 1;
+    const long long ih = it / PARTS >> 1, grp = ih >> 31 ? ih / a.H : (long long)((uint32_t)ih / (uint32_t)a.H);
     const int h = (int)(ih - grp * a.H);
     const long long t0 = grp * 16;
     const KvGroup s = kv_group<FMT, D>(a, w, ROPE ? &rope : nullptr, t0);
@@ -573,198 +572,214 @@ __global__ void __launch_bounds__(KV_THREADS, D <= 128 ? 12 : 8)
     if (!is_v) {
       KvRow kr[2];
       const uint16_t *x[2];
+      const float *tab[2] = {nullptr, nullptr};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         kr[k] = kv_row(s, g + 8 * k);
         x[k] = w.k + (t0 + kr[k].i) * w.ks + (size_t)h * D;
+        if (ROPE && kr[k].unit >= 0) tab[k] = rope.table + (size_t)rope.pos[t0 + kr[k].i] * rope.rot;
       }
-      uint4 kx[2][NB];
+      auto key = [&](int k, int b, float *f) {  // octet 4 b + t of key k as fp32
+        if (kr[k].unit < 0) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          kx[k][b] = !ROPE && kr[k].unit >= 0 ? *reinterpret_cast<const uint4 *>(x[k] + 32 * b + 8 * t) : make_uint4(0, 0, 0, 0);
-      auto keys = [&](int k, float (&f)[NB][8]) {  // the lane's octets of key k as fp32
-        if constexpr (ROPE) {
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[b][i] = 0.f;
-          if (kr[k].unit >= 0)
-            rope_octets<NB>(x[k], t, rope.rot, rope.inter, rope.table + (size_t)rope.pos[t0 + kr[k].i] * rope.rot, f);
+          for (int i = 0; i < 8; ++i) f[i] = 0.f;
+        } else if constexpr (ROPE) {
+          rope_octet(x[k], 4 * b + t, rope.rot, rope.inter, tab[k], f);
         } else {
-#pragma unroll
-          for (int b = 0; b < NB; ++b) unpack8(kx[k][b], f[b]);
+          unpack8(*reinterpret_cast<const uint4 *>(x[k] + 32 * b + 8 * t), f);
         }
       };
       const bool whole = s.run && kr[0].unit == kr[1].unit;
       if constexpr (FMT == A_BF16) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          if constexpr (ROPE) {
-            float f[NB][8];
-            keys(k, f);
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int b = 0; b < NB; ++b) kx[k][b] = pack8(f[b]);
+          for (int k = 0; k < 2; ++k) {
+            const int b = 2 * part + j;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if constexpr (ROPE) {
+              float f[8];
+              key(k, b, f);
+              v = pack8(f);
+            } else if (kr[k].unit >= 0) {
+              v = *reinterpret_cast<const uint4 *>(x[k] + 32 * b + 8 * t);
+            }
+            if (kr[k].unit >= 0) *reinterpret_cast<uint4 *>(base + kr[k].unit + k_octet<GS>(4 * b + t, kr[k].row)) = v;
           }
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            if (kr[k].unit >= 0)
-              *reinterpret_cast<uint4 *>(base + kr[k].unit + k_octet<GS>(4 * b + t, kr[k].row)) = kx[k][b];
-        }
       } else if constexpr (FMT == A_FP8) {
-        uint2 c[2][NB];
+        // Up to 128 channels a row stays in registers.  Beyond, the second pass
+        // reads it again (from L1) and rotates it again, in a loop that is not
+        // unrolled: the body would outgrow the instruction cache.
+        constexpr bool KEEP = D <= 128;
+        float f[2][KEEP ? NB : 1][8], amax[2] = {0.f, 0.f};
+        auto octet = [&](int k, int b) { return f[k][KEEP ? b : 0]; };
+#pragma unroll(KEEP ? NB : 1)
+        for (int b = 0; b < NB; ++b) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            key(k, b, octet(k, b));
+            amax[k] = fmaxf(amax[k], amax8(octet(k, b)));
+          }
+        }
+        Divisor sc[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float amax = 0.f, f[NB][8];
-          keys(k, f);
-#pragma unroll
-          for (int b = 0; b < NB; ++b) amax = fmaxf(amax, amax8(f[b]));
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-          const Divisor sc = divisor(e4m3_scale(amax), amax);
-#pragma unroll
-          for (int b = 0; b < NB; ++b) c[k][b] = e4m3_octet(f[b], sc);
-          if (t == 0 && kr[k].unit >= 0) reinterpret_cast<float *>(base + kr[k].unit + 2 * CB)[kr[k].row] = sc.d;
+          amax[k] = fmaxf(amax[k], __shfl_xor_sync(0xffffffffu, amax[k], 1));
+          amax[k] = fmaxf(amax[k], __shfl_xor_sync(0xffffffffu, amax[k], 2));
+          sc[k] = divisor(e4m3_scale(amax[k]), amax[k]);
+          if (t == 0 && kr[k].unit >= 0) reinterpret_cast<float *>(base + kr[k].unit + 2 * CB)[kr[k].row] = sc[k].d;
         }
-#pragma unroll
+#pragma unroll(KEEP ? NB : 1)
         for (int b = 0; b < NB; ++b) {
+          uint2 c[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            if (!KEEP) key(k, b, octet(k, b));
+            c[k] = e4m3_octet(octet(k, b), sc[k]);
+          }
           if (whole) {
-            *reinterpret_cast<uint4 *>(base + kr[0].unit + (b * 32 + lane) * 16) =
-                make_uint4(c[0][b].x, c[0][b].y, c[1][b].x, c[1][b].y);
+            *reinterpret_cast<uint4 *>(base + kr[0].unit + (b * 32 + lane) * 16) = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
           } else {
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-              if (kr[k].unit >= 0)
-                *reinterpret_cast<uint2 *>(base + kr[k].unit + k_octet<GS>(4 * b + t, kr[k].row)) = c[k][b];
+              if (kr[k].unit >= 0) *reinterpret_cast<uint2 *>(base + kr[k].unit + k_octet<GS>(4 * b + t, kr[k].row)) = c[k];
           }
         }
       } else {
         const float gl = a.glob[0];
         const Divisor gd = divisor(gl, 0.f);
-        uint32_t c[2][NB];
+        const int b = 2 * part;
+        uint32_t c[2][2], sb[2][2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float f[NB][8];
-          keys(k, f);
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            float amax = amax8(f[b]);
+          for (int k = 0; k < 2; ++k) {
+            float f[8];
+            key(k, b + j, f);
+            float amax = amax8(f);
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            const uint32_t sb = nvfp4_scale(amax, gd);
-            c[k][b] = nvfp4_octet(f[b], sb, gl, amax);
-            if ((t & 1) == 0 && kr[k].unit >= 0)
-              base[kr[k].unit + 2 * CB + kr[k].row * (D / 16) + (t >> 1) * NB + b] = (uint8_t)sb;
+            sb[j][k] = nvfp4_scale(amax, gd);
+            c[j][k] = nvfp4_octet(f, sb[j][k], gl, amax);
           }
-        }
 #pragma unroll
-        for (int b = 0; b < NB; b += 2) {
-          if (whole) {
-            *reinterpret_cast<uint4 *>(base + kr[0].unit + (b * 16 + lane) * 16) =
-                make_uint4(c[0][b], c[1][b], c[0][b + 1], c[1][b + 1]);
-          } else {
+        for (int k = 0; k < 2; ++k)  // the blocks of octets b and b + 1 are neighbours
+          if ((t & 1) == 0 && kr[k].unit >= 0)
+            *reinterpret_cast<uint16_t *>(base + kr[k].unit + 2 * CB + kr[k].row * (D / 16) + (t >> 1) * NB + b) =
+                (uint16_t)(sb[0][k] | sb[1][k] << 8);
+        if (whole) {
+          *reinterpret_cast<uint4 *>(base + kr[0].unit + (b * 16 + lane) * 16) = make_uint4(c[0][0], c[0][1], c[1][0], c[1][1]);
+        } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (kr[k & 1].unit >= 0)
-                *reinterpret_cast<uint32_t *>(base + kr[k & 1].unit + k_octet<GS>(4 * (b + (k >> 1)) + t, kr[k & 1].row)) =
-                    c[k & 1][b + (k >> 1)];
-          }
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              if (kr[k].unit >= 0)
+                *reinterpret_cast<uint32_t *>(base + kr[k].unit + k_octet<GS>(4 * (b + j) + t, kr[k].row)) = c[j][k];
         }
       }
       continue;
     }
 
     KvRow vr[4];
-    uint4 vx[4][NQ];
+    const uint16_t *x[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       vr[k] = kv_row(s, 2 * t + (k & 1) + 8 * (k >> 1));
-      const uint16_t *x = w.v + (t0 + vr[k].i) * w.vs + (size_t)h * D + g * (D / 8);
-#pragma unroll
-      for (int q = 0; q < NQ; ++q)
-        vx[k][q] = vr[k].unit >= 0 ? *reinterpret_cast<const uint4 *>(x + 8 * q) : make_uint4(0, 0, 0, 0);
+      x[k] = w.v + (t0 + vr[k].i) * w.vs + (size_t)h * D;
     }
+    auto value = [&](int k, int o) {  // octet o of value k
+      return vr[k].unit >= 0 ? *reinterpret_cast<const uint4 *>(x[k] + 8 * o) : make_uint4(0, 0, 0, 0);
+    };
     if constexpr (FMT == A_BF16) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int q = 0; q < NQ; ++q)
-          if (vr[k].unit >= 0)
-            *reinterpret_cast<uint4 *>(base + vr[k].unit + CB + v_octet<GS, D>(g * NQ + q, vr[k].row)) = vx[k][q];
+      for (int k = 0; k < 4; ++k) {
+        const uint4 v = value(k, g * NQ + part);
+        if (vr[k].unit >= 0)
+          *reinterpret_cast<uint4 *>(base + vr[k].unit + CB + v_octet<GS, D>(g * NQ + part, vr[k].row)) = v;
+      }
     } else if constexpr (FMT == A_FP8) {
-      uint2 c[4][NQ];
+      constexpr bool KEEP = D <= 128;  // as for the keys
+      uint4 row[4][KEEP ? NQ : 1];
+      float amax[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll(KEEP ? NQ : 1)
+      for (int q = 0; q < NQ; ++q) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) row[k][KEEP ? q : 0] = value(k, g * NQ + q);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float f[8];
+          unpack8(row[k][KEEP ? q : 0], f);
+          amax[k] = fmaxf(amax[k], amax8(f));
+        }
+      }
+      Divisor sc[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        float amax = 0.f, f[8];
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          unpack8(vx[k][q], f);
-          amax = fmaxf(amax, amax8(f));
-        }
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const Divisor sc = divisor(e4m3_scale(amax), amax);
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          unpack8(vx[k][q], f);
-          c[k][q] = e4m3_octet(f, sc);
-        }
-        if (g == 0 && vr[k].unit >= 0) reinterpret_cast<float *>(base + vr[k].unit + 2 * CB + SB)[vr[k].row] = sc.d;
+        for (int o = 4; o < 32; o <<= 1) amax[k] = fmaxf(amax[k], __shfl_xor_sync(0xffffffffu, amax[k], o));
+        sc[k] = divisor(e4m3_scale(amax[k]), amax[k]);
+        if (g == 0 && vr[k].unit >= 0) reinterpret_cast<float *>(base + vr[k].unit + 2 * CB + SB)[vr[k].row] = sc[k].d;
       }
+#pragma unroll(KEEP ? NQ : 1)
+      for (int q = 0; q < NQ; ++q) {
+        uint2 c[4];
 #pragma unroll
-      for (int k = 0; k < 4; k += 2) {
-        const bool whole = s.run && vr[k].unit == vr[k + 1].unit;
+        for (int k = 0; k < 4; ++k) {
+          float f[8];
+          unpack8(KEEP ? row[k][KEEP ? q : 0] : value(k, g * NQ + q), f);
+          c[k] = e4m3_octet(f, sc[k]);
+        }
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          if (whole) {
+        for (int k = 0; k < 4; k += 2) {
+          if (s.run && vr[k].unit == vr[k + 1].unit) {
             *reinterpret_cast<uint4 *>(base + vr[k].unit + CB + ((q * 2 + k / 2) * 32 + lane) * 16) =
-                make_uint4(c[k][q].x, c[k][q].y, c[k + 1][q].x, c[k + 1][q].y);
+                make_uint4(c[k].x, c[k].y, c[k + 1].x, c[k + 1].y);
           } else {
 #pragma unroll
             for (int j = k; j < k + 2; ++j)
               if (vr[j].unit >= 0)
-                *reinterpret_cast<uint2 *>(base + vr[j].unit + CB + v_octet<GS, D>(g * NQ + q, vr[j].row)) = c[j][q];
+                *reinterpret_cast<uint2 *>(base + vr[j].unit + CB + v_octet<GS, D>(g * NQ + q, vr[j].row)) = c[j];
           }
         }
       }
     } else {
       const float gl = a.glob[1];
       const Divisor gd = divisor(gl, 0.f);
-      uint32_t c[4][NQ];
+      const bool whole = s.run && vr[0].unit == vr[1].unit && vr[0].unit == vr[2].unit && vr[0].unit == vr[3].unit;
+      const int o = g * NQ + part;
+      uint4 mine[4], next[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        float am[NQ];
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          float f[8];
-          unpack8(vx[k][q], f);
-          am[q] = amax8(f);
-        }
-        // a block is octets 2j and 2j + 1: neighbours in the lane, or the lane's last and the next one's first
-        const float over = __shfl_xor_sync(0xffffffffu, (g & 1) ? am[0] : am[NQ - 1], 4);
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          const int o = g * NQ + q, qq = q + ((o & 1) ? -1 : 1);  // the block's other octet
-          const float amax = fmaxf(am[q], qq >= 0 && qq < NQ ? am[(qq + NQ) % NQ] : over);
-          const uint32_t sb = nvfp4_scale(amax, gd);
-          float f[8];
-          unpack8(vx[k][q], f);
-          c[k][q] = nvfp4_octet(f, sb, gl, amax);
-          if ((o & 1) == 0 && vr[k].unit >= 0) base[vr[k].unit + 2 * CB + SB + (o >> 1) * 16 + vr[k].row] = (uint8_t)sb;
-        }
+        mine[k] = value(k, o);
+        next[k] = value(k, o ^ 1);  // the block's other octet
       }
-      const bool whole = s.run && vr[0].unit == vr[1].unit && vr[0].unit == vr[2].unit && vr[0].unit == vr[3].unit;
+      uint32_t c[4], sb[4];
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) {
+      for (int k = 0; k < 4; ++k) {
+        float f[8], other[8];
+        unpack8(mine[k], f);
+        unpack8(next[k], other);
+        const float amax = fmaxf(amax8(f), amax8(other));
+        sb[k] = nvfp4_scale(amax, gd);
+        c[k] = nvfp4_octet(f, sb[k], gl, amax);
+      }
+      if ((o & 1) == 0) {
+        const size_t at = 2 * CB + SB + (o >> 1) * 16;
         if (whole) {
-          *reinterpret_cast<uint4 *>(base + vr[0].unit + CB + (q * 32 + lane) * 16) =
-              make_uint4(c[0][q], c[1][q], c[2][q], c[3][q]);
+          *reinterpret_cast<uint16_t *>(base + vr[0].unit + at + 2 * t) = (uint16_t)(sb[0] | sb[1] << 8);
+          *reinterpret_cast<uint16_t *>(base + vr[0].unit + at + 2 * t + 8) = (uint16_t)(sb[2] | sb[3] << 8);
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (vr[k].unit >= 0)
-              *reinterpret_cast<uint32_t *>(base + vr[k].unit + CB + v_octet<GS, D>(g * NQ + q, vr[k].row)) = c[k][q];
+            if (vr[k].unit >= 0) base[vr[k].unit + at + vr[k].row] = (uint8_t)sb[k];
         }
+      }
+      if (whole) {
+        *reinterpret_cast<uint4 *>(base + vr[0].unit + CB + (part * 32 + lane) * 16) = make_uint4(c[0], c[1], c[2], c[3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (vr[k].unit >= 0) *reinterpret_cast<uint32_t *>(base + vr[k].unit + CB + v_octet<GS, D>(o, vr[k].row)) = c[k];
       }
     }
   }
@@ -976,14 +991,15 @@ static hq_status kv_dispatch(int fmt, int D, F &&f) {
   return HQ_ERR_UNSUPPORTED;
 }
 
-static int kv_blocks(const KvArgs &a, const KvRows &w) {
-  const long long work = (((long long)w.T + 15) / 16 * a.H * 2 + KV_THREADS / 32 - 1) / (KV_THREADS / 32);
-  return (int)(work < 148 * 12 ? work : 148 * 12);
+// Blocks of two warps, no more than the SMs hold at a time.
+static int kv_blocks(long long warps) {
+  const long long blocks = (warps + KV_THREADS / 32 - 1) / (KV_THREADS / 32);
+  return (int)(blocks < 148 * 12 ? blocks : 148 * 12);
 }
 
 hq_status launch_kv_write(int fmt, int D, const KvArgs &a, const KvRows &w, const RopeArgs &rope, cudaStream_t st) {
   return kv_dispatch(fmt, D, [&](auto F, auto DD) {
-    const int kb = kv_blocks(a, w);
+    const int kb = kv_blocks(((long long)w.T + 15) / 16 * a.H * 2 * kv_parts(F, DD));
     if (rope.rot) {
       // A step's q is rotated by further blocks of the launch; a prompt's by
       // the rotation's own kernel, whose blocks are four times as many to an SM
@@ -1004,7 +1020,7 @@ hq_status launch_kv_write(int fmt, int D, const KvArgs &a, const KvRows &w, cons
 
 hq_status launch_kv_read(int fmt, int D, const KvArgs &a, const KvRows &w, cudaStream_t st) {
   return kv_dispatch(fmt, D, [&](auto F, auto DD) {
-    kv_read_kernel<F, DD><<<kv_blocks(a, w), KV_THREADS, 0, st>>>(a, w);
+    kv_read_kernel<F, DD><<<kv_blocks(((long long)w.T + 15) / 16 * a.H * 2), KV_THREADS, 0, st>>>(a, w);
     return check_launch();
   });
 }
