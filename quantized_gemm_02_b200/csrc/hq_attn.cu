@@ -114,7 +114,8 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 
 // ---- shape of a kernel ---------------------------------------------------------
 // NT = 8-head tiles per item.  W consumer warps, each with a ring of STAGES
-// units, and one producer warp.  A partial record is GT x D normalised outputs
+// units, and P producer warps (a lane's copies are issued one after the
+// other, some 150 cycles each: one producer held NVFP4 caches at 60% of HBM).  A partial record is GT x D normalised outputs
 // and GT log2 sums; a warp leaves at most two: one in its drained ring, the
 // other, written while the ring is in use, beside the rings or, where records
 // are large, in the workspace (so in L2).
@@ -128,13 +129,14 @@ struct AttnShape {
   static constexpr int PART = GT * (D + 4) * 4;  // bytes; the sums padded to 16 per head
   static constexpr bool FAR = GT * D >= 2048;    // first records in the workspace
   static constexpr int fit(int w) { return ((ATTN_SMEM - ATTN_HEAD) / w - (FAR ? 0 : PART)) / UNIT; }
-  // The producer makes W + 1 warps a multiple of four, one per scheduler: 16
-  // warps may have 128 registers a lane, 12 168 and 8 or 4 255.  Of the counts that the registers
-  // allow (6 per output tile and 16 channels, and some 70 more), the largest
-  // that keeps 120 KB on its way.
+  // W + P warps are a multiple of four, one per scheduler: 16 warps may have
+  // 128 registers a lane, 12 168 and 8 or 4 255.  Of the counts that the
+  // registers allow (6 per output tile and 16 channels, and some 70 more), the
+  // largest that keeps 120 KB on its way.
   static constexpr int REGS = NT * (D / 16) * 6;
   static constexpr bool deep(int w) { return fit(w) >= 2 && w * fit(w) * UNIT >= 120 * 1024; }
-  static constexpr int W = REGS <= 48 && deep(15) ? 15 : REGS <= 96 && deep(11) ? 11 : deep(7) ? 7 : 3;
+  static constexpr int W = REGS <= 48 && deep(14) ? 14 : REGS <= 96 && deep(10) ? 10 : deep(7) ? 7 : 3;
+  static constexpr int P = W >= 10 ? 2 : 1;
   static constexpr int STAGES = fit(W) < 12 ? fit(W) : 12;
   static constexpr int SMEM = ATTN_HEAD + W * ((FAR ? 0 : PART) + STAGES * UNIT);
   static constexpr size_t workspace(int sms) {  // after the counters
@@ -205,15 +207,15 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {  // 
 }
 
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + 32, 1) attn_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT, D, NT>::P * 32, 1) attn_kernel(AttnArgs a) {
   using S = AttnShape<FMT, D, NT>;
-  constexpr int W = S::W, STAGES = S::STAGES, UNIT = S::UNIT, GT = S::GT, PART = S::PART;
+  constexpr int W = S::W, P = S::P, STAGES = S::STAGES, UNIT = S::UNIT, GT = S::GT, PART = S::PART;
   constexpr int CB = kv_code_bytes(FMT, D), SB = kv_scale_bytes(FMT, D);
-  constexpr int THREADS = W * 32 + 32;
+  constexpr int THREADS = (W + P) * 32;
   constexpr bool BF = FMT == A_BF16;
   constexpr float LIM = BF ? 8.f : 15.f, SHIFT = BF ? 0.f : 10.f;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_scan[W + 1];
+  __shared__ long long s_scan[W + P];
   __shared__ int s_last[2], s_from[4];
   __shared__ float s_lse[GT];
   __shared__ volatile int s_stop;
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + 32, 1) attn_ke
   __syncthreads();
   long long before = incl - mine, sum = 0;
 #pragma unroll
-  for (int w = 0; w <= W; ++w) {
+  for (int w = 0; w < W + P; ++w) {
     if (w < warp) before += s_scan[w];
     sum += s_scan[w];
   }
@@ -273,8 +275,8 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + 32, 1) attn_ke
   if ((int)blockIdx.x >= ctas) return;
   const long long c_begin = attn_div(blockIdx.x * total, ctas);
   const long long c_units = attn_div((blockIdx.x + 1) * total, ctas) - c_begin;
-  // this warp's units (producer: lane w has warp w's)
-  const int wi = warp < W ? warp : min(lane, W);
+  // this warp's units (producer p: lane i has warp i P + p's)
+  const int wi = warp < W ? warp : min(lane * P + warp - W, W);
   const long long w_begin = wi * c_units / W;
   int left = wi < W ? (int)((wi + 1) * c_units / W - w_begin) : 0;
   __syncthreads();
@@ -296,8 +298,8 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + 32, 1) attn_ke
     pw.u = (int)(off - (long long)pw.it * pw.nu);
   }
 
-  if (warp == W) {
-    // The producer: lane w walks consumer warp w's part of the line.
+  if (warp >= W) {
+    // A producer: each lane walks one consumer warp's part of the line.
     int to_issue = left, issued = 0, stage = 0, pidx = 0, psub = 0, pg = 0;
     uint32_t parity = 1;
     const int upp = a.kv.page_units;
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + 32, 1) attn_ke
     if (to_issue > 0) locate();
     unsigned long long idle = 0;
     while (__any_sync(0xffffffffu, to_issue > 0)) {
-      const int slot = lane * STAGES + stage;
+      const int slot = wi * STAGES + stage;
       const bool ready = to_issue > 0 && (issued < STAGES || mbar_test(&head->empty[slot], parity));
       if (ready) {
         const int tok0 = (pw.u0 + pw.u) * 16;
@@ -726,7 +728,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + 32, 1) attn_ke
   {
     const unsigned upto = (2u << lane) - 1u, after = starts & ~upto;
     const int run = 31 - __clz(starts & upto), run_end = after ? __ffs(after) - 2 : 31;
-    for (int hl = warp; hl < GT; hl += W + 1) {
+    for (int hl = warp; hl < GT; hl += W + P) {
       const float ls = fl & 1 ? record(lane)[GT * D + hl * 4] : -INFINITY;
       float m = ls;
 #pragma unroll
@@ -824,7 +826,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + 32, 1) attn_ke
     float *w = reinterpret_cast<float *>(smem + ATTN_HEAD);  // [n][GT], where the rings were
     for (int i = tid; i < GT * n; i += THREADS) w[i] = __ldcg(rec(i / GT) + GT * D + i % GT * 4);
     __syncthreads();
-    for (int hl = warp; hl < GT; hl += W + 1) {
+    for (int hl = warp; hl < GT; hl += W + P) {
       float m = -INFINITY, s = 0.f;
       for (int c = lane; c < n; c += 32) m = fmaxf(m, w[c * GT + hl]);
 #pragma unroll
@@ -878,7 +880,7 @@ static hq_status attn_start(const AttnArgs &a, int sms, cudaStream_t st) {
       return HQ_ERR_CUDA;
     if (dev < 32) configured |= 1u << dev;
   }
-  attn_kernel<FMT, D, NT><<<sms, S::W * 32 + 32, S::SMEM, st>>>(a);
+  attn_kernel<FMT, D, NT><<<sms, (S::W + S::P) * 32, S::SMEM, st>>>(a);
   return check_launch();
 }
 
