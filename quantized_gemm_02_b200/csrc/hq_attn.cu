@@ -71,10 +71,12 @@ __device__ __forceinline__ int attn_range(const AttnArgs &a, int b, int &first) 
   first = a.window > 0 && n > a.window ? n - a.window : 0;
   return n;
 }
-__device__ __forceinline__ int attn_units(const AttnArgs &a, int b) {
+// Steps of TOK tokens, aligned to multiples of TOK in the sequence.
+template <int TOK>
+__device__ __forceinline__ int attn_steps(const AttnArgs &a, int b) {
   int first;
   const int n = attn_range(a, b, first);
-  return n ? (int)(((long long)n + 15) / 16) - first / 16 : 0;
+  return n ? (int)(((long long)n + TOK - 1) / TOK) - first / TOK : 0;
 }
 
 // ---- fragments ---------------------------------------------------------------
@@ -111,6 +113,18 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+template <bool BF>  // the first of a chain: c = A B
+__device__ __forceinline__ void mma16816_new(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {
+  if constexpr (BF)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 
 // ---- shape of a kernel ---------------------------------------------------------
 // NT = 8-head tiles per item.  W consumer warps, each with a ring of STAGES
@@ -126,28 +140,31 @@ template <int FMT, int D, int NT>
 struct AttnShape {
   static constexpr int GT = 8 * NT;
   static constexpr int UNIT = kv_unit_bytes(FMT, D);
+  // A step is one unit, or two of the small ones: half the handshakes and
+  // copies, and two independent chains of MMAs.
+  static constexpr int STEP = FMT == A_NVFP4 || UNIT <= 2304 ? 2 : 1, TOK = 16 * STEP, BYTES = STEP * UNIT;
   static constexpr int PART = GT * (D + 4) * 4;  // bytes; the sums padded to 16 per head
   static constexpr bool FAR = GT * D >= 2048;    // first records in the workspace
-  static constexpr int fit(int w) { return ((ATTN_SMEM - ATTN_HEAD) / w - (FAR ? 0 : PART)) / UNIT; }
+  static constexpr int fit(int w) { return ((ATTN_SMEM - ATTN_HEAD) / w - (FAR ? 0 : PART)) / BYTES; }
   // W + P warps are a multiple of four, one per scheduler: 16 warps may have
   // 128 registers a lane, 12 168 and 8 or 4 255.  Of the counts that the
   // registers allow (6 per output tile and 16 channels, and some 70 more), the
   // largest that keeps 120 KB on its way.
   static constexpr int REGS = NT * (D / 16) * 6;
-  static constexpr bool deep(int w) { return fit(w) >= 2 && w * fit(w) * UNIT >= 120 * 1024; }
+  static constexpr bool deep(int w) { return fit(w) >= 2 && w * fit(w) * BYTES >= 120 * 1024; }
   static constexpr int W = REGS <= 48 && deep(14) ? 14 : REGS <= 96 && deep(10) ? 10 : deep(7) ? 7 : 3;
   static constexpr int P = W >= 10 ? 2 : 1;
   static constexpr int STAGES = fit(W) < 12 ? fit(W) : 12;
-  static constexpr int SMEM = ATTN_HEAD + W * ((FAR ? 0 : PART) + STAGES * UNIT);
+  static constexpr int SMEM = ATTN_HEAD + W * ((FAR ? 0 : PART) + STAGES * BYTES);
   static constexpr size_t workspace(int sms) {  // after the counters
     return (size_t)sms * PART * (2 + (FAR ? W : 0));
   }
-  static_assert(STAGES >= 2 && STAGES * UNIT >= PART && W * STAGES * UNIT >= GT * ATTN_MAX_CTAS * 4, "ring too small");
+  static_assert(STAGES >= 2 && STAGES * BYTES >= PART && W * STAGES * BYTES >= GT * ATTN_MAX_CTAS * 4, "ring too small");
 };
 constexpr int ATTN_RINGS = 15 * 12;  // most (warp, stage) pairs
 
-struct AttnUnit {        // what the producer says of a unit
-  int b, it, u, nu;      // sequence, head group, the unit's place in its item and the item's units
+struct AttnUnit {        // what the producer says of a step
+  int b, it, u, nu;      // sequence, head group, the step's place in its item and the item's steps
 };
 struct AttnSeg {         // a part of an item that a warp leaves behind
   long long start;       // the item's first unit in the line
@@ -158,18 +175,19 @@ struct AttnSeg {         // a part of an item that a warp leaves behind
 struct AttnHead {
   uint64_t full[ATTN_RINGS], empty[ATTN_RINGS];
   AttnUnit unit[ATTN_RINGS];
-  int meta[ATTN_RINGS];  // valid tokens [lo, hi) in bits 0..4 and 5..9, and flags:
+  int meta[ATTN_RINGS];  // valid tokens [lo, hi) in bits 0..5 and 6..11, and flags:
   AttnSeg seg[30];       // [W][2]
   long long before[512]; // units of the sequences before a thread's share
 };
-enum { ATTN_LAST = 1024, ATTN_BAD = 2048 };  // the item's last unit; a page that does not exist
-// A walk along the line of units.
+enum { ATTN_LAST = 1 << 12, ATTN_BAD = 1 << 13 };  // the item's last step; unit k's page does not exist (BAD << k)
+// A walk along the line of steps.
+template <int TOK>
 struct AttnWalk {
   int b, it, u, nu, u0, len, first;
   __device__ __forceinline__ void open(const AttnArgs &a) {
     len = attn_range(a, b, first);
-    u0 = first / 16;
-    nu = len ? (int)(((long long)len + 15) / 16) - u0 : 0;
+    u0 = first / TOK;
+    nu = len ? (int)(((long long)len + TOK - 1) / TOK) - u0 : 0;
   }
   // to the next unit; there is one.  True if it is another item's.
   __device__ __forceinline__ bool next(const AttnArgs &a, int items) {
@@ -210,6 +228,7 @@ template <int FMT, int D, int NT>
 __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT, D, NT>::P * 32, 1) attn_kernel(AttnArgs a) {
   using S = AttnShape<FMT, D, NT>;
   constexpr int W = S::W, P = S::P, STAGES = S::STAGES, UNIT = S::UNIT, GT = S::GT, PART = S::PART;
+  constexpr int STEP = S::STEP, TOK = S::TOK, BYTES = S::BYTES;
   constexpr int CB = kv_code_bytes(FMT, D), SB = kv_scale_bytes(FMT, D);
   constexpr int THREADS = (W + P) * 32;
   constexpr bool BF = FMT == A_BF16;
@@ -225,7 +244,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
   const int items = a.kv.H * a.hgroups;
   auto near_record = [&](int w) {  // a warp's part of an item begun before
     return S::FAR ? a.parts + ((size_t)gridDim.x * 2 + (size_t)blockIdx.x * W + w) * (PART / 4)
-                  : reinterpret_cast<float *>(smem + ATTN_HEAD + W * STAGES * UNIT) + w * (PART / 4);
+                  : reinterpret_cast<float *>(smem + ATTN_HEAD + W * STAGES * BYTES) + w * (PART / 4);
   };
 
   if (tid < W * STAGES) {
@@ -242,7 +261,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
   long long mine = 0;
   for (int k = 0; k < per; ++k) {
     const int b = tid * per + k;
-    const int n = b < a.B ? attn_units(a, b) : 1;
+    const int n = b < a.B ? attn_steps<TOK>(a, b) : 1;
     if (b < a.B) mine += n;
     unsigned empty = __ballot_sync(0xffffffffu, n == 0 && b % gridDim.x == blockIdx.x);
     while (empty) {
@@ -280,7 +299,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
   const long long w_begin = wi * c_units / W;
   int left = wi < W ? (int)((wi + 1) * c_units / W - w_begin) : 0;
   __syncthreads();
-  AttnWalk pw{};  // where they begin
+  AttnWalk<TOK> pw{};  // where they begin
   if (left > 0) {
     const long long at = c_begin + w_begin, seq = attn_div(at, items);
     const int shares = (a.B + per - 1) / per;
@@ -300,33 +319,71 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
 
   if (warp >= W) {
     // A producer: each lane walks one consumer warp's part of the line.
-    int to_issue = left, issued = 0, stage = 0, pidx = 0, psub = 0, pg = 0;
+    int to_issue = left, issued = 0, stage = 0, pidx = 0, psub = 0, pg[STEP] = {};
     uint32_t parity = 1;
     const int upp = a.kv.page_units;
-    auto locate = [&]() {
-      pidx = (pw.u0 + pw.u) / upp;
-      psub = (pw.u0 + pw.u) - pidx * upp;
-      pg = a.page_table[(size_t)pw.b * a.max_pages + pidx];
+    const int32_t *pages = a.page_table;
+    // The pages of the step's units.  Entries before the window or past the
+    // length are not used; the second unit may be on the next page.
+    auto fetch = [&](bool turned) {
+      if (turned) {
+        pages = a.page_table + (size_t)pw.b * a.max_pages;
+        pidx = (pw.u0 + pw.u) * STEP / upp;
+        psub = (pw.u0 + pw.u) * STEP - pidx * upp;
+      } else {
+        psub += STEP;
+        if (psub < upp) {
+          if (STEP == 1 || psub + 1 < upp) {
+            if (STEP == 2) pg[1] = pg[0];
+            return;
+          }
+        } else {
+          psub -= upp;
+          ++pidx;
+          if (STEP == 2 && psub >= upp) {  // pages of one unit
+            psub -= upp;
+            ++pidx;
+          }
+        }
+      }
+      const int at = (pw.u0 + pw.u) * TOK;
+      pg[0] = STEP == 1 || at + 16 > pw.first ? pages[pidx] : -1;
+      if constexpr (STEP == 2) pg[1] = at + 16 >= pw.len ? -1 : psub + 1 < upp ? pages[pidx] : pages[pidx + 1];
     };
-    if (to_issue > 0) locate();
+    if (to_issue > 0) fetch(true);
     unsigned long long idle = 0;
     while (__any_sync(0xffffffffu, to_issue > 0)) {
       const int slot = wi * STAGES + stage;
       const bool ready = to_issue > 0 && (issued < STAGES || mbar_test(&head->empty[slot], parity));
       if (ready) {
-        const int tok0 = (pw.u0 + pw.u) * 16;
-        const bool ok = pg >= 0 && pg < a.num_pages;
+        const int tok0 = (pw.u0 + pw.u) * TOK, lo = max(pw.first - tok0, 0), hi = min(pw.len - tok0, TOK);
+        int meta = lo | hi << 6 | (pw.u + 1 == pw.nu ? ATTN_LAST : 0), bytes = 0;
+        bool go[STEP];
+#pragma unroll
+        for (int k = 0; k < STEP; ++k) {
+          const bool used = lo < 16 * k + 16 && hi > 16 * k;
+          go[k] = used && pg[k] >= 0 && pg[k] < a.num_pages;
+          if (used && !go[k]) {
+            meta |= ATTN_BAD << k;
+            set_device_error(HQ_ERR_DEVICE_INDEX);
+          }
+          if (go[k]) bytes += UNIT;
+        }
         head->unit[slot] = AttnUnit{pw.b, pw.it, pw.u, pw.nu};
-        head->meta[slot] = max(pw.first - tok0, 0) | min(pw.len - tok0, 16) << 5 | (pw.u + 1 == pw.nu ? ATTN_LAST : 0) |
-                           (ok ? 0 : ATTN_BAD);
-        if (ok) {
-          const uint8_t *src = a.kv.pages + (size_t)pg * a.kv.page_bytes +
-                               ((size_t)(pw.it / a.hgroups) * upp + psub) * UNIT;
-          mbar_arrive_expect_tx(&head->full[slot], UNIT);
-          bulk_g2s(smem + ATTN_HEAD + slot * UNIT, src, UNIT, &head->full[slot]);
+        head->meta[slot] = meta;
+        const size_t head_off = (size_t)(pw.it / a.hgroups) * upp;
+        uint8_t *dst = smem + ATTN_HEAD + slot * BYTES;
+        const uint8_t *src = a.kv.pages + (size_t)pg[0] * a.kv.page_bytes + (head_off + psub) * UNIT;
+        if (bytes) mbar_arrive_expect_tx(&head->full[slot], bytes);
+        else mbar_arrive(&head->full[slot]);
+        if constexpr (STEP == 1) {
+          if (bytes) bulk_g2s(dst, src, UNIT, &head->full[slot]);
+        } else if (bytes == BYTES && psub + 1 < upp) {
+          bulk_g2s(dst, src, BYTES, &head->full[slot]);
         } else {
-          set_device_error(HQ_ERR_DEVICE_INDEX);
-          mbar_arrive(&head->full[slot]);
+          const int sub = psub + 1 < upp ? psub + 1 : 0;
+          if (go[0]) bulk_g2s(dst, src, UNIT, &head->full[slot]);
+          if (go[1]) bulk_g2s(dst + UNIT, a.kv.pages + (size_t)pg[1] * a.kv.page_bytes + (head_off + sub) * UNIT, UNIT, &head->full[slot]);
         }
         ++issued;
         if (++stage == STAGES) {
@@ -334,12 +391,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
           parity ^= 1u;
         }
         if (--to_issue > 0) {
-          if (pw.next(a, items)) {
-            locate();
-          } else if (++psub == upp) {
-            psub = 0;
-            pg = a.page_table[(size_t)pw.b * a.max_pages + ++pidx];
-          }
+          fetch(pw.next(a, items));
         }
       }
       if (__any_sync(0xffffffffu, ready)) {
@@ -356,7 +408,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
   }
   if (warp < W && left > 0) {
     long long pos = c_begin + w_begin;  // the next unit, along the line
-    uint8_t *ring = smem + ATTN_HEAD + warp * (STAGES * UNIT);
+    uint8_t *ring = smem + ATTN_HEAD + warp * (STAGES * BYTES);
     float *rec0 = near_record(warp);
     AttnUnit cu{pw.b, pw.it, pw.u, pw.nu};  // the item at hand
     long long item_start = pos - pw.u;
@@ -447,201 +499,239 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
         break;
       }
       const int meta = head->meta[slot];
-      if (!(meta & ATTN_BAD)) {
-        uint8_t *unit = ring + stage * UNIT;
-        const uint4 *kv4 = reinterpret_cast<const uint4 *>(unit) + lane;
-        const uint4 *vv4 = reinterpret_cast<const uint4 *>(unit + CB) + lane;
-        const uint8_t *ksc = unit + 2 * CB, *vsc = ksc + SB;
-        const int lo = meta & 31, hi = meta >> 5 & 31;  // valid tokens
-        const bool edge = lo > 0 || hi < 16;
+      {
+        uint8_t *unit = ring + stage * BYTES;
+        const int lo = meta & 63, hi = meta >> 6 & 63;  // valid tokens
+        const bool edge = lo > 0 || hi < TOK || meta >= ATTN_BAD;
+        auto valid = [&](int j) { return j >= lo && j < hi && !(meta & ATTN_BAD << (j >> 4)); };
         if (edge) {
           // what lies past the sequence may be NaN, and 0 * NaN is: zero the values this lane reads
-          auto valid = [&](int tk) {  // token of the lane's value octets
-            const int j = 2 * t + (tk & 1) + 8 * (tk >> 1);
-            return j >= lo && j < hi;
-          };
           constexpr int GS = kv_granule(FMT);
+#pragma unroll 1
+          for (int k = 0; k < STEP; ++k) {
+            uint8_t *v = unit + k * UNIT + CB;
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            if (valid(i & 3)) continue;
-            uint8_t *p = unit + CB + lane_byte<GS>(lane, i);
-            if constexpr (FMT == A_BF16) *reinterpret_cast<uint4 *>(p) = make_uint4(0, 0, 0, 0);
-            if constexpr (FMT == A_FP8) *reinterpret_cast<uint2 *>(p) = make_uint2(0, 0);
-            if constexpr (FMT == A_NVFP4) *reinterpret_cast<uint32_t *>(p) = 0;
-          }
-          if constexpr (FMT == A_NVFP4) {
-            for (int i = lane; i < D; i += 32)
-              if ((i & 15) < lo || (i & 15) >= hi) unit[2 * CB + SB + i] = 0;
+            for (int i = 0; i < D / 16; ++i) {
+              if (valid(16 * k + 2 * t + (i & 1) + 8 * ((i >> 1) & 1))) continue;
+              uint8_t *p = v + lane_byte<GS>(lane, i);
+              if constexpr (FMT == A_BF16) *reinterpret_cast<uint4 *>(p) = make_uint4(0, 0, 0, 0);
+              if constexpr (FMT == A_FP8) *reinterpret_cast<uint2 *>(p) = make_uint2(0, 0);
+              if constexpr (FMT == A_NVFP4) *reinterpret_cast<uint32_t *>(p) = 0;
+            }
+            if constexpr (FMT == A_NVFP4) {
+              for (int i = lane; i < D; i += 32)
+                if (!valid(16 * k + (i & 15))) v[CB + SB + i] = 0;
+            }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
         }
 
-        // S^T: rows g and g + 8 (tokens) x heads 2t, 2t + 1
+        // S^T of unit k: rows g and g + 8 (tokens) x heads 2t, 2t + 1.  One unit
+        // takes two chains of MMAs, two take one each.
         float acc[NT][2][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int k = 0; k < STEP; ++k) {
+          const uint4 *kv4 = reinterpret_cast<const uint4 *>(unit + k * UNIT) + lane;
+          auto qk = [&](int step, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[nt][0][j] = acc[nt][1][j] = 0.f;
-        auto qk = [&](int step, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+            for (int nt = 0; nt < NT; ++nt) {
+              if (step < (STEP == 2 ? 1 : 2))
+                mma16816_new<BF>(acc[nt][STEP == 2 ? k : step & 1], a0, a1, a2, a3, qf[nt][step][0], qf[nt][step][1]);
+              else
+                mma16816<BF>(acc[nt][STEP == 2 ? k : step & 1], a0, a1, a2, a3, qf[nt][step][0], qf[nt][step][1]);
+            }
+          };
+          if constexpr (FMT == A_BF16) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816<BF>(acc[nt][step & 1], a0, a1, a2, a3, qf[nt][step][0], qf[nt][step][1]);
-        };
-        float kscale[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
-        if constexpr (FMT == A_BF16) {
+            for (int b = 0; b < D / 32; ++b) {
+              const uint4 v0 = kv4[(2 * b) * 32], v1 = kv4[(2 * b + 1) * 32];
+              qk(2 * b, v0.x, v1.x, v0.y, v1.y);
+              qk(2 * b + 1, v0.z, v1.z, v0.w, v1.w);
+            }
+          } else if constexpr (FMT == A_FP8) {
 #pragma unroll
-          for (int b = 0; b < D / 32; ++b) {
-            const uint4 v0 = kv4[(2 * b) * 32], v1 = kv4[(2 * b + 1) * 32];
-            qk(2 * b, v0.x, v1.x, v0.y, v1.y);
-            qk(2 * b + 1, v0.z, v1.z, v0.w, v1.w);
-          }
-        } else if constexpr (FMT == A_FP8) {
-          kscale[0] = reinterpret_cast<const float *>(ksc)[g];
-          kscale[1] = reinterpret_cast<const float *>(ksc)[g + 8];
-          lv[0] = lg2(reinterpret_cast<const float *>(vsc)[g]);
-          lv[1] = lg2(reinterpret_cast<const float *>(vsc)[g + 8]);
+            for (int b = 0; b < D / 32; ++b) {
+              const uint4 v = kv4[b * 32];
+              qk(2 * b, e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.z >> 16));
+              qk(2 * b + 1, e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.y >> 16),
+                 e4m3x2_to_f16x2(v.w >> 16));
+            }
+          } else {
+            // this lane's channels 32b + 8t.. lie in 16-channel block 2b + t / 2
+            const uint8_t *ksc = unit + k * UNIT + 2 * CB;
+            const uint16_t *s0 = reinterpret_cast<const uint16_t *>(ksc + g * (D / 16) + (t >> 1) * (D / 32));
+            const uint16_t *s1 = reinterpret_cast<const uint16_t *>(ksc + (g + 8) * (D / 16) + (t >> 1) * (D / 32));
 #pragma unroll
-          for (int b = 0; b < D / 32; ++b) {
-            const uint4 v = kv4[b * 32];
-            qk(2 * b, e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.z >> 16));
-            qk(2 * b + 1, e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.y >> 16),
-               e4m3x2_to_f16x2(v.w >> 16));
-          }
-        } else {
-          // this lane's channels 32b + 8t.. lie in 16-channel block 2b + t / 2
-          const uint16_t *s0 = reinterpret_cast<const uint16_t *>(ksc + g * (D / 16) + (t >> 1) * (D / 32));
-          const uint16_t *s1 = reinterpret_cast<const uint16_t *>(ksc + (g + 8) * (D / 16) + (t >> 1) * (D / 32));
-#pragma unroll
-          for (int b2 = 0; b2 < D / 64; ++b2) {
-            const uint4 v = kv4[b2 * 32];
-            const uint32_t p0 = e4m3x2_to_f16x2(s0[b2]), p1 = e4m3x2_to_f16x2(s1[b2]);
-            const uint32_t r0 = __byte_perm(p0, 0, 0x1010), r1 = __byte_perm(p1, 0, 0x1010);
-            const uint32_t t0 = __byte_perm(p0, 0, 0x3232), t1 = __byte_perm(p1, 0, 0x3232);
-            qk(4 * b2, hmul2(e2m1x2_to_f16x2<0>(v.x), r0), hmul2(e2m1x2_to_f16x2<0>(v.y), r1),
-               hmul2(e2m1x2_to_f16x2<1>(v.x), r0), hmul2(e2m1x2_to_f16x2<1>(v.y), r1));
-            qk(4 * b2 + 1, hmul2(e2m1x2_to_f16x2<2>(v.x), r0), hmul2(e2m1x2_to_f16x2<2>(v.y), r1),
-               hmul2(e2m1x2_to_f16x2<3>(v.x), r0), hmul2(e2m1x2_to_f16x2<3>(v.y), r1));
-            qk(4 * b2 + 2, hmul2(e2m1x2_to_f16x2<0>(v.z), t0), hmul2(e2m1x2_to_f16x2<0>(v.w), t1),
-               hmul2(e2m1x2_to_f16x2<1>(v.z), t0), hmul2(e2m1x2_to_f16x2<1>(v.w), t1));
-            qk(4 * b2 + 3, hmul2(e2m1x2_to_f16x2<2>(v.z), t0), hmul2(e2m1x2_to_f16x2<2>(v.w), t1),
-               hmul2(e2m1x2_to_f16x2<3>(v.z), t0), hmul2(e2m1x2_to_f16x2<3>(v.w), t1));
+            for (int b2 = 0; b2 < D / 64; ++b2) {
+              const uint4 v = kv4[b2 * 32];
+              const uint32_t p0 = e4m3x2_to_f16x2(s0[b2]), p1 = e4m3x2_to_f16x2(s1[b2]);
+              const uint32_t r0 = __byte_perm(p0, 0, 0x1010), r1 = __byte_perm(p1, 0, 0x1010);
+              const uint32_t t0 = __byte_perm(p0, 0, 0x3232), t1 = __byte_perm(p1, 0, 0x3232);
+              qk(4 * b2, hmul2(e2m1x2_to_f16x2<0>(v.x), r0), hmul2(e2m1x2_to_f16x2<0>(v.y), r1),
+                 hmul2(e2m1x2_to_f16x2<1>(v.x), r0), hmul2(e2m1x2_to_f16x2<1>(v.y), r1));
+              qk(4 * b2 + 1, hmul2(e2m1x2_to_f16x2<2>(v.x), r0), hmul2(e2m1x2_to_f16x2<2>(v.y), r1),
+                 hmul2(e2m1x2_to_f16x2<3>(v.x), r0), hmul2(e2m1x2_to_f16x2<3>(v.y), r1));
+              qk(4 * b2 + 2, hmul2(e2m1x2_to_f16x2<0>(v.z), t0), hmul2(e2m1x2_to_f16x2<0>(v.w), t1),
+                 hmul2(e2m1x2_to_f16x2<1>(v.z), t0), hmul2(e2m1x2_to_f16x2<1>(v.w), t1));
+              qk(4 * b2 + 3, hmul2(e2m1x2_to_f16x2<2>(v.z), t0), hmul2(e2m1x2_to_f16x2<2>(v.w), t1),
+                 hmul2(e2m1x2_to_f16x2<3>(v.z), t0), hmul2(e2m1x2_to_f16x2<3>(v.w), t1));
+            }
           }
         }
 
-        // softmax weights.  x: scores, y: scores + log2 of the value's scale (E4M3)
-        float x[NT][4], y[NT][4];
+        // Scores above the reference, in base 2.  x: of the weight; y (E4M3):
+        // of the weight times the value's scale, which has its own reference.
+        float x[NT][STEP][4], y[NT][STEP][4];
         bool raise = false;
+        const float *scales = reinterpret_cast<const float *>(unit + 2 * CB);  // E4M3: keys' [16], values' [16]
+        auto sum = [&](int nt, int k, int j) { return STEP == 2 ? acc[nt][k][j] : acc[nt][0][j] + acc[nt][1][j]; };
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int k = 0; k < STEP; ++k) {
+          float kscale[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
+          if constexpr (FMT == A_FP8) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float s = (acc[nt][0][j] + acc[nt][1][j]) * qc[nt][j & 1];
-            if constexpr (FMT == A_FP8) s *= kscale[j >> 1];
-            float sv = s + lv[j >> 1];
-            if (edge) {
-              const int tk = g + 8 * (j >> 1);
-              if (tk < lo || tk >= hi) s = sv = -INFINITY;
+            for (int r = 0; r < 2; ++r) {
+              kscale[r] = scales[k * (UNIT / 4) + g + 8 * r];
+              lv[r] = lg2(scales[k * (UNIT / 4) + 16 + g + 8 * r]);
             }
-            x[nt][j] = s;
-            y[nt][j] = sv;
-            if constexpr (FMT == A_FP8) raise |= s > ref[nt][j & 1] + 64.f || sv > refv[nt][j & 1] + LIM;
-            else raise |= s > ref[nt][j & 1] + LIM;
           }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if constexpr (FMT == A_FP8) {
+                const float sq = sum(nt, k, j) * (qc[nt][j & 1] * kscale[j >> 1]);
+                x[nt][k][j] = sq - ref[nt][j & 1];
+                y[nt][k][j] = sq + (lv[j >> 1] - refv[nt][j & 1]);
+              } else {
+                x[nt][k][j] = __fmaf_rn(sum(nt, k, j), qc[nt][j & 1], -ref[nt][j & 1]);
+              }
+              if (edge && !valid(16 * k + g + 8 * (j >> 1))) x[nt][k][j] = y[nt][k][j] = -INFINITY;
+              raise |= x[nt][k][j] > (FMT == A_FP8 ? 64.f : LIM);
+              if constexpr (FMT == A_FP8) raise |= y[nt][k][j] > LIM;
+            }
+        }
         if (__any_sync(0xffffffffu, raise)) {
+          // Move the references up to the step's largest score.  The scores are
+          // formed again: the first reference, -3e38, has swallowed them.
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              float mx = fmaxf(x[nt][j], x[nt][2 + j]), mv = fmaxf(y[nt][j], y[nt][2 + j]);
+              float sx[2 * STEP], sy[2 * STEP], mx = -INFINITY, mv = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < 2 * STEP; ++i) {
+                const int k = i >> 1, r = i & 1;
+                const bool out = x[nt][k][2 * r + j] == -INFINITY;  // masked
+                float q = qc[nt][j], lv = 0.f;
+                if constexpr (FMT == A_FP8) {
+                  q *= scales[k * (UNIT / 4) + g + 8 * r];
+                  lv = lg2(scales[k * (UNIT / 4) + 16 + g + 8 * r]);
+                }
+                sx[i] = out ? -INFINITY : sum(nt, k, 2 * r + j) * q;
+                sy[i] = out ? -INFINITY : sx[i] + lv;
+                mx = fmaxf(mx, sx[i]);
+                mv = fmaxf(mv, sy[i]);
+              }
 #pragma unroll
               for (int k = 4; k < 32; k <<= 1) {
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
                 if constexpr (FMT == A_FP8) mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, k));
               }
               const float r = fmaxf(ref[nt][j], mx - (FMT == A_FP8 ? 0.f : SHIFT));
-              const float keep = ex2(ref[nt][j] - r);
+              float keep = ex2(ref[nt][j] - r);
               ref[nt][j] = r;
               l[nt][j] *= keep;
-              float ko = keep;
               if constexpr (FMT == A_FP8) {
                 const float rv = fmaxf(refv[nt][j], mv - SHIFT);
-                ko = ex2(refv[nt][j] - rv);
+                keep = ex2(refv[nt][j] - rv);
                 refv[nt][j] = rv;
               }
 #pragma unroll
+              for (int i = 0; i < 2 * STEP; ++i) {
+                x[nt][i >> 1][2 * (i & 1) + j] = sx[i] - ref[nt][j];
+                y[nt][i >> 1][2 * (i & 1) + j] = sy[i] - refv[nt][j];
+              }
+#pragma unroll
               for (int i = 0; i < D / 16; ++i) {
-                o[nt][i][j] *= ko;
-                o[nt][i][2 + j] *= ko;
+                o[nt][i][j] *= keep;
+                o[nt][i][2 + j] *= keep;
               }
             }
         }
-        uint32_t pb[NT][2], pl[NT][2];  // B fragments of P^T: tokens 2t, 2t + 1 (+ 8), head g
+        uint32_t pb[NT][STEP][2], pl[NT][STEP][2];  // B fragments of P^T: tokens 2t, 2t + 1 (+ 8), head g
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float p[4], w[4];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            p[j] = ex2(x[nt][j] - ref[nt][j & 1]);
-            w[j] = FMT == A_FP8 ? ex2(y[nt][j] - refv[nt][j & 1]) : p[j];
-          }
-          l[nt][0] += p[0] + p[2];
-          l[nt][1] += p[1] + p[3];
+          for (int k = 0; k < STEP; ++k) {
+            float p[4], w[4];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            if constexpr (BF) {
-              const uint32_t hi2 = bf16x2(w[2 * r], w[2 * r + 1]);
-              pb[nt][r] = transpose8(hi2);
-              pl[nt][r] = transpose8(bf16x2(w[2 * r] - bf16_lo(hi2), w[2 * r + 1] - bf16_hi(hi2)));
-            } else {
-              pb[nt][r] = transpose8(f16x2(w[2 * r], w[2 * r + 1]));
+            for (int j = 0; j < 4; ++j) {
+              p[j] = ex2(x[nt][k][j]);
+              w[j] = FMT == A_FP8 ? ex2(y[nt][k][j]) : p[j];
+            }
+            l[nt][0] += p[0] + p[2];
+            l[nt][1] += p[1] + p[3];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              if constexpr (BF) {
+                const uint32_t hi2 = bf16x2(w[2 * r], w[2 * r + 1]);
+                pb[nt][k][r] = transpose8(hi2);
+                pl[nt][k][r] = transpose8(bf16x2(w[2 * r] - bf16_lo(hi2), w[2 * r + 1] - bf16_hi(hi2)));
+              } else {
+                pb[nt][k][r] = transpose8(f16x2(w[2 * r], w[2 * r + 1]));
+              }
             }
           }
-        }
 
         // O^T: rows g and g + 8 are channels g (D / 8) + 2i and + 1
-        auto pv = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma16816<BF>(o[nt][i], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-            if constexpr (BF) mma16816<BF>(o[nt][i], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
-          }
-        };
+        for (int k = 0; k < STEP; ++k) {
+          const uint4 *vv4 = reinterpret_cast<const uint4 *>(unit + k * UNIT + CB) + lane;
+          auto pv = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
-        for (int q = 0; q < D / 64; ++q) {
-          if constexpr (FMT == A_BF16) {
-            const uint4 v0 = vv4[(4 * q) * 32], v1 = vv4[(4 * q + 1) * 32], v2 = vv4[(4 * q + 2) * 32],
-                        v3 = vv4[(4 * q + 3) * 32];
-            const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w},
-                           w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              pv(4 * q + i, __byte_perm(w0[i], w1[i], 0x5410), __byte_perm(w0[i], w1[i], 0x7632),
-                 __byte_perm(w2[i], w3[i], 0x5410), __byte_perm(w2[i], w3[i], 0x7632));
-          } else if constexpr (FMT == A_FP8) {
-            const uint4 v0 = vv4[(2 * q) * 32], v1 = vv4[(2 * q + 1) * 32];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t a = __byte_perm(i < 2 ? v0.x : v0.y, i < 2 ? v0.z : v0.w, (i & 1) ? 0x7362 : 0x5140);
-              const uint32_t c = __byte_perm(i < 2 ? v1.x : v1.y, i < 2 ? v1.z : v1.w, (i & 1) ? 0x7362 : 0x5140);
-              pv(4 * q + i, e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(c), e4m3x2_to_f16x2(c >> 16));
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816<BF>(o[nt][i], a0, a1, a2, a3, pb[nt][k][0], pb[nt][k][1]);
+              if constexpr (BF) mma16816<BF>(o[nt][i], a0, a1, a2, a3, pl[nt][k][0], pl[nt][k][1]);
             }
-          } else {
-            const uint4 v = vv4[q * 32];
-            const int blk = (g * (D / 64) + q) >> 1;
-            const uint16_t *vs = reinterpret_cast<const uint16_t *>(vsc + blk * 16);
-            const uint32_t s01 = e4m3x2_to_f16x2(vs[t]), s23 = e4m3x2_to_f16x2(vs[t + 4]);
-            const uint32_t m = 0x0f0f0f0fu;
-            const uint32_t e0 = (v.x & m) | ((v.y & m) << 4), e1 = ((v.x >> 4) & m) | (v.y & ~m);
-            const uint32_t e2 = (v.z & m) | ((v.w & m) << 4), e3 = ((v.z >> 4) & m) | (v.w & ~m);
-            pv(4 * q, hmul2(e2m1x2_to_f16x2<0>(e0), s01), hmul2(e2m1x2_to_f16x2<0>(e1), s01),
-               hmul2(e2m1x2_to_f16x2<0>(e2), s23), hmul2(e2m1x2_to_f16x2<0>(e3), s23));
-            pv(4 * q + 1, hmul2(e2m1x2_to_f16x2<1>(e0), s01), hmul2(e2m1x2_to_f16x2<1>(e1), s01),
-               hmul2(e2m1x2_to_f16x2<1>(e2), s23), hmul2(e2m1x2_to_f16x2<1>(e3), s23));
-            pv(4 * q + 2, hmul2(e2m1x2_to_f16x2<2>(e0), s01), hmul2(e2m1x2_to_f16x2<2>(e1), s01),
-               hmul2(e2m1x2_to_f16x2<2>(e2), s23), hmul2(e2m1x2_to_f16x2<2>(e3), s23));
-            pv(4 * q + 3, hmul2(e2m1x2_to_f16x2<3>(e0), s01), hmul2(e2m1x2_to_f16x2<3>(e1), s01),
-               hmul2(e2m1x2_to_f16x2<3>(e2), s23), hmul2(e2m1x2_to_f16x2<3>(e3), s23));
+          };
+#pragma unroll
+          for (int q = 0; q < D / 64; ++q) {
+            if constexpr (FMT == A_BF16) {
+              const uint4 v0 = vv4[(4 * q) * 32], v1 = vv4[(4 * q + 1) * 32], v2 = vv4[(4 * q + 2) * 32],
+                          v3 = vv4[(4 * q + 3) * 32];
+              const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w},
+                             w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                pv(4 * q + i, __byte_perm(w0[i], w1[i], 0x5410), __byte_perm(w0[i], w1[i], 0x7632),
+                   __byte_perm(w2[i], w3[i], 0x5410), __byte_perm(w2[i], w3[i], 0x7632));
+            } else if constexpr (FMT == A_FP8) {
+              const uint4 v0 = vv4[(2 * q) * 32], v1 = vv4[(2 * q + 1) * 32];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t a = __byte_perm(i < 2 ? v0.x : v0.y, i < 2 ? v0.z : v0.w, (i & 1) ? 0x7362 : 0x5140);
+                const uint32_t c = __byte_perm(i < 2 ? v1.x : v1.y, i < 2 ? v1.z : v1.w, (i & 1) ? 0x7362 : 0x5140);
+                pv(4 * q + i, e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(c), e4m3x2_to_f16x2(c >> 16));
+              }
+            } else {
+              const uint4 v = vv4[q * 32];
+              const int blk = (g * (D / 64) + q) >> 1;
+              const uint16_t *vs = reinterpret_cast<const uint16_t *>(unit + k * UNIT + 2 * CB + SB + blk * 16);
+              const uint32_t s01 = e4m3x2_to_f16x2(vs[t]), s23 = e4m3x2_to_f16x2(vs[t + 4]);
+              const uint32_t m = 0x0f0f0f0fu;
+              const uint32_t e0 = (v.x & m) | ((v.y & m) << 4), e1 = ((v.x >> 4) & m) | (v.y & ~m);
+              const uint32_t e2 = (v.z & m) | ((v.w & m) << 4), e3 = ((v.z >> 4) & m) | (v.w & ~m);
+              pv(4 * q, hmul2(e2m1x2_to_f16x2<0>(e0), s01), hmul2(e2m1x2_to_f16x2<0>(e1), s01),
+                 hmul2(e2m1x2_to_f16x2<0>(e2), s23), hmul2(e2m1x2_to_f16x2<0>(e3), s23));
+              pv(4 * q + 1, hmul2(e2m1x2_to_f16x2<1>(e0), s01), hmul2(e2m1x2_to_f16x2<1>(e1), s01),
+                 hmul2(e2m1x2_to_f16x2<1>(e2), s23), hmul2(e2m1x2_to_f16x2<1>(e3), s23));
+              pv(4 * q + 2, hmul2(e2m1x2_to_f16x2<2>(e0), s01), hmul2(e2m1x2_to_f16x2<2>(e1), s01),
+                 hmul2(e2m1x2_to_f16x2<2>(e2), s23), hmul2(e2m1x2_to_f16x2<2>(e3), s23));
+              pv(4 * q + 3, hmul2(e2m1x2_to_f16x2<3>(e0), s01), hmul2(e2m1x2_to_f16x2<3>(e1), s01),
+                 hmul2(e2m1x2_to_f16x2<3>(e2), s23), hmul2(e2m1x2_to_f16x2<3>(e3), s23));
+            }
           }
         }
       }
@@ -714,7 +804,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
   const unsigned present = __ballot_sync(0xffffffffu, fl & 1), begin = __ballot_sync(0xffffffffu, fl & 2),
                  end = __ballot_sync(0xffffffffu, fl & 4), starts = begin | 1u;
   auto record = [&](int e) {
-    return e & 1 ? reinterpret_cast<const float *>(smem + ATTN_HEAD + (e >> 1) * (STAGES * UNIT)) : near_record(e >> 1);
+    return e & 1 ? reinterpret_cast<const float *>(smem + ATTN_HEAD + (e >> 1) * (STAGES * BYTES)) : near_record(e >> 1);
   };
   auto finish = [&](const AttnSeg &sg, int hl, int d, float4 v, float lse2) {  // 4 channels of one head
     const int hq = (sg.it % a.hgroups) * GT + hl;
