@@ -134,7 +134,7 @@ __device__ __forceinline__ void mma16816_new(float (&c)[4], uint32_t a0, uint32_
 // other, written while the ring is in use, beside the rings or, where records
 // are large, in the workspace (so in L2).
 constexpr int ATTN_SMEM = 227 * 1024 - 1024;  // what a CTA may have, less the static part
-constexpr int ATTN_HEAD = 11520;              // barriers and bookkeeping
+constexpr int ATTN_HEAD = 9728;               // barriers and bookkeeping
 constexpr int ATTN_MAX_CTAS = 256;
 template <int FMT, int D, int NT>
 struct AttnShape {
@@ -159,7 +159,7 @@ struct AttnShape {
   static constexpr size_t workspace(int sms) {  // after the counters
     return (size_t)sms * PART * (2 + (FAR ? W : 0));
   }
-  static_assert(STAGES >= 2 && STAGES * BYTES >= PART && W * STAGES * BYTES >= GT * ATTN_MAX_CTAS * 4, "ring too small");
+  static_assert(STAGES >= 2 && STAGES * BYTES >= PART, "ring too small");
 };
 constexpr int ATTN_RINGS = 15 * 12;  // most (warp, stage) pairs
 
@@ -167,17 +167,30 @@ struct AttnUnit {        // what the producer says of a step
   int b, it, u, nu;      // sequence, head group, the step's place in its item and the item's steps
 };
 struct AttnSeg {         // a part of an item that a warp leaves behind
-  long long start;       // the item's first unit in the line
+  int start;             // the item's first step in the line
   int b, it, nu;
-  int flags;             // 1: present, 2: holds the item's first unit, 4: its last
+  int flags;             // 1: present, 2: holds the item's first step, 4: its last
+};
+
+struct AttnRun {         // segments of one item
+  unsigned members;
+  int first, begins, ends;
 };
 
 struct AttnHead {
   uint64_t full[ATTN_RINGS], empty[ATTN_RINGS];
-  AttnUnit unit[ATTN_RINGS];
-  int meta[ATTN_RINGS];  // valid tokens [lo, hi) in bits 0..5 and 6..11, and flags:
-  AttnSeg seg[30];       // [W][2]
-  long long before[512]; // units of the sequences before a thread's share
+  union {
+    struct {                   // while units are streamed
+      AttnUnit unit[ATTN_RINGS];
+      int before[512];         // steps of the sequences before a thread's share
+    };
+    struct {                   // then, of the join
+      float weight[16 * 32], run_lse[16 * 32];
+    };
+  };
+  AttnRun run[30];
+  int meta[ATTN_RINGS];        // valid tokens [lo, hi) in bits 0..5 and 6..11, and flags:
+  AttnSeg seg[30];             // [W][2]
 };
 enum { ATTN_LAST = 1 << 12, ATTN_BAD = 1 << 13 };  // the item's last step; unit k's page does not exist (BAD << k)
 // A walk along the line of steps.
@@ -203,15 +216,17 @@ struct AttnWalk {
   }
 };
 
-// n / d, in 32 bits where both fit (a 64-bit division is some hundred cycles)
-__device__ __forceinline__ long long attn_div(long long n, long long d) {
-  return (n | d) >> 32 ? n / d : (long long)((uint32_t)n / (uint32_t)d);
-}
-// CTA c of `ctas` has the units from floor(c total / ctas) on; the CTA of unit u
-__device__ __forceinline__ int attn_cta_of(long long u, long long total, int ctas) {
-  return (int)attn_div((u + 1) * ctas - 1, total);
-}
+// n things in `parts` consecutive parts that differ by one at most.
+struct AttnSplit {
+  int each, more;  // the first `more` parts have one more
+  __device__ __forceinline__ int begin(int part) const { return part * each + min(part, more); }
+  __device__ __forceinline__ int part_of(int i) const {
+    const int n = more * (each + 1);
+    return i < n ? i / (each + 1) : more + (i - n) / each;
+  }
+};
 
+__device__ __forceinline__ unsigned upto_mask(int lane) { return (2u << lane) - 1u; }
 __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {  // does not suspend the warp
   uint32_t ok;
   asm volatile(
@@ -234,9 +249,8 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
   constexpr bool BF = FMT == A_BF16;
   constexpr float LIM = BF ? 8.f : 15.f, SHIFT = BF ? 0.f : 10.f;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_scan[W + P];
-  __shared__ int s_last[2], s_from[4];
-  __shared__ float s_lse[GT];
+  __shared__ unsigned s_scan[W + P];
+  __shared__ int s_last[2], s_from[6];
   __shared__ volatile int s_stop;
   AttnHead *head = reinterpret_cast<AttnHead *>(smem);
   static_assert(sizeof(AttnHead) <= ATTN_HEAD && W * STAGES <= ATTN_RINGS, "bookkeeping");
@@ -258,11 +272,12 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
   // The line's length: each thread counts the units of its share of the
   // sequences.  Empty sequences get their zeros from one of the CTAs.
   const int per = (a.B + THREADS - 1) / THREADS;
-  long long mine = 0;
+  unsigned mine = 0;
   for (int k = 0; k < per; ++k) {
     const int b = tid * per + k;
     const int n = b < a.B ? attn_steps<TOK>(a, b) : 1;
-    if (b < a.B) mine += n;
+    // (32 bits hold the line, or the call is refused below; a share stops short of wrapping around)
+    if (b < a.B) mine = min(mine + (unsigned)n, 1u << 30);
     unsigned empty = __ballot_sync(0xffffffffu, n == 0 && b % gridDim.x == blockIdx.x);
     while (empty) {
       const int eb = __shfl_sync(0xffffffffu, b, __ffs(empty) - 1);
@@ -273,48 +288,51 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
         for (int i = lane; i < a.q_heads; i += 32) a.lse[(size_t)eb * a.q_heads + i] = -INFINITY;
     }
   }
-  long long incl = mine;
+  unsigned incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+    const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl = min(incl + v, 1u << 30);
   }
   if (lane == 31) s_scan[warp] = incl;
   __syncthreads();
-  long long before = incl - mine, sum = 0;
-#pragma unroll
-  for (int w = 0; w < W + P; ++w) {
+  const int shares = (a.B + per - 1) / per;
+  unsigned long long before = incl - mine, sum = 0;
+  for (int w = 0; w * 32 < shares; ++w) {
     if (w < warp) before += s_scan[w];
     sum += s_scan[w];
   }
-  head->before[tid] = before;
-  const long long total = sum * items;
-  const long long want = (total + W - 1) / W;  // a unit per warp at least
-  const int ctas = (int)(want < gridDim.x ? want : gridDim.x);
+  head->before[tid] = (int)before;
+  if (sum * items >= 1ull << 30) {  // steps are counted in 32 bits
+    if (tid == 0) set_device_error(HQ_ERR_UNSUPPORTED);
+    return;
+  }
+  const int total = (int)sum * items;
+  const int ctas = min((total + W - 1) / W, (int)gridDim.x);  // a step per warp at least
   if ((int)blockIdx.x >= ctas) return;
-  const long long c_begin = attn_div(blockIdx.x * total, ctas);
-  const long long c_units = attn_div((blockIdx.x + 1) * total, ctas) - c_begin;
-  // this warp's units (producer p: lane i has warp i P + p's)
+  const int each = total / ctas;
+  const AttnSplit line{each, total - each * ctas};
+  const int c_begin = line.begin(blockIdx.x), c_steps = line.begin(blockIdx.x + 1) - c_begin;
+  // this warp's steps (producer p: lane i has warp i P + p's)
   const int wi = warp < W ? warp : min(lane * P + warp - W, W);
-  const long long w_begin = wi * c_units / W;
-  int left = wi < W ? (int)((wi + 1) * c_units / W - w_begin) : 0;
+  const AttnSplit mine_of{c_steps / W, c_steps % W};
+  const int w_begin = c_begin + mine_of.begin(wi);
+  int left = wi < W ? mine_of.each + (wi < mine_of.more) : 0;
   __syncthreads();
   AttnWalk<TOK> pw{};  // where they begin
   if (left > 0) {
-    const long long at = c_begin + w_begin, seq = attn_div(at, items);
-    const int shares = (a.B + per - 1) / per;
-    int lo = 0;  // the last share that begins at or before `at`
-    for (int o = 1 << 8; o > 0; o >>= 1)
+    const int seq = w_begin / items;
+    int lo = 0;  // the last share that begins at or before it
+    for (int o = shares > 1 ? 1 << (31 - __clz(shares - 1)) : 0; o > 0; o >>= 1)
       if (lo + o < shares && head->before[lo + o] <= seq) lo += o;
-    long long off = at - head->before[lo] * items;
+    int off = w_begin - head->before[lo] * items;
     for (pw.b = lo * per;; ++pw.b) {
       pw.open(a);
-      const long long n = (long long)pw.nu * items;
-      if (off < n) break;
-      off -= n;
+      if (off < pw.nu * items) break;
+      off -= pw.nu * items;
     }
-    pw.it = (int)attn_div(off, pw.nu);
-    pw.u = (int)(off - (long long)pw.it * pw.nu);
+    pw.it = off / pw.nu;
+    pw.u = off - pw.it * pw.nu;
   }
 
   if (warp >= W) {
@@ -407,11 +425,11 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
     }
   }
   if (warp < W && left > 0) {
-    long long pos = c_begin + w_begin;  // the next unit, along the line
+    int pos = w_begin;  // the next step, along the line
     uint8_t *ring = smem + ATTN_HEAD + warp * (STAGES * BYTES);
     float *rec0 = near_record(warp);
     AttnUnit cu{pw.b, pw.it, pw.u, pw.nu};  // the item at hand
-    long long item_start = pos - pw.u;
+    int item_start = pos - pw.u;
     uint32_t qf[NT][D / 16][2];  // B fragments of q: k = this lane's channels, n = head g
     float qc[NT][2];             // score multiplier of heads 2t, 2t + 1
     float o[NT][D / 16][4], l[NT][2], ref[NT][2], refv[NT][2];
@@ -424,7 +442,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
       auto arrived = [&]() { return __all_sync(0xffffffffu, mbar_wait(&head->full[slot], parity)); };
       if (fresh) {  // the first item is known before its unit is here
         fresh = false;
-        if (pos != c_begin + w_begin && arrived()) {
+        if (pos != w_begin && arrived()) {
           cu = head->unit[slot];
           item_start = pos - cu.u;
         }
@@ -746,7 +764,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
       ++pos;
 
       if ((meta & ATTN_LAST) || left == 0) {  // the item, or this warp's part of it, is done
-        const bool begins = item_start >= c_begin + w_begin, ends = meta & ATTN_LAST;
+        const bool begins = item_start >= w_begin, ends = meta & ATTN_LAST;
         const int h = cu.it / a.hgroups, hg = cu.it % a.hgroups;
         float *rec = begins ? reinterpret_cast<float *>(ring) : rec0;
 #pragma unroll
@@ -814,10 +832,15 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
     if (a.lse && d == 0) a.lse[(size_t)sg.b * a.q_heads + row] = lse2 * 0.6931471805599453f;
   };
   // each segment's weight and each run's log2 sum, by scans within the runs
-  float *weight = reinterpret_cast<float *>(head->before), *run_lse = weight + GT * 32;  // [GT][32]
+  int runs;
   {
     const unsigned upto = (2u << lane) - 1u, after = starts & ~upto;
     const int run = 31 - __clz(starts & upto), run_end = after ? __ffs(after) - 2 : 31;
+    const unsigned members = present & upto_mask(run_end) & ~((1u << run) - 1u);
+    const unsigned heads = __ballot_sync(0xffffffffu, lane == run && members);
+    runs = __popc(heads);
+    if (warp == 0 && (heads >> lane & 1u))
+      head->run[__popc(heads & (upto >> 1))] = AttnRun{members, __ffs(members) - 1, (int)(begin >> lane & 1u), (end & members) != 0};
     for (int hl = warp; hl < GT; hl += W + P) {
       const float ls = fl & 1 ? record(lane)[GT * D + hl * 4] : -INFINITY;
       float m = ls;
@@ -835,113 +858,115 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
         if (lane - o >= run) s += u;
       }
       s = __shfl_sync(0xffffffffu, s, run_end);
-      weight[hl * 32 + lane] = s == 0.f ? 0.f : w / s;
-      if (lane == run) run_lse[hl * 32 + lane] = s == 0.f ? -INFINITY : r + lg2(s);
+      head->weight[hl * 32 + lane] = s == 0.f ? 0.f : __fdividef(w, s);
+      if (lane == run) head->run_lse[hl * 32 + lane] = s == 0.f ? -INFINITY : r + lg2(s);
     }
   }
   __syncthreads();
-  // Records that stay in the workspace: [0] of an item begun before this CTA,
-  // [1] of one that goes on after it.
-  int open0 = -1, open1 = -1;  // a segment of theirs
-  for (unsigned todo = starts; todo; todo &= todo - 1) {
-    const int e0 = __ffs(todo) - 1;
-    const unsigned next = todo & (todo - 1);
-    const unsigned members = present & ~((1u << e0) - 1u) & (next ? (next & -next) - 1u : ~0u);
-    if (!members) continue;
-    const int first = __ffs(members) - 1;
-    const bool begins = begin >> e0 & 1u, ends = end & members;
-    const AttnSeg sg = head->seg[first];
-    float *to = a.parts + ((size_t)blockIdx.x * 2 + begins) * (PART / 4);
-    for (int x = tid; x < GT * D / 4; x += THREADS) {
-      const int hl = x / (D / 4), d = (x % (D / 4)) * 4;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (unsigned mm = members; mm;) {
-        float w[4];
-        float4 p[4];
+  // All runs at once, 4 channels of a head at a time.  What spans CTAs goes to
+  // the workspace: record [0] of an item begun before this CTA (the first run),
+  // [1] of one that goes on after it (the last).
+  constexpr int QUADS = GT * D / 4;
+  for (int i = tid; i < runs * QUADS; i += THREADS) {
+    const int rn = i / QUADS, x = i - rn * QUADS, hl = x / (D / 4), d = (x % (D / 4)) * 4;
+    const AttnRun run = head->run[rn];
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (unsigned mm = run.members; mm;) {
+      float w[2];
+      float4 p[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int e = mm ? __ffs(mm) - 1 : first;
-          w[k] = mm ? weight[hl * 32 + e] : 0.f;
-          p[k] = *reinterpret_cast<const float4 *>(record(e) + hl * D + d);
-          mm &= mm - 1;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v.x += w[k] * p[k].x; v.y += w[k] * p[k].y; v.z += w[k] * p[k].z; v.w += w[k] * p[k].w;
-        }
+      for (int k = 0; k < 2; ++k) {
+        const int e = mm ? __ffs(mm) - 1 : run.first;
+        w[k] = mm ? head->weight[hl * 32 + e] : 0.f;
+        p[k] = *reinterpret_cast<const float4 *>(record(e) + hl * D + d);
+        mm &= mm - 1;
       }
-      const float lse2 = run_lse[hl * 32 + e0];
-      if (begins && ends) {
-        finish(sg, hl, d, v, lse2);
-      } else {
-        __stcg(reinterpret_cast<float4 *>(to + hl * D + d), v);
-        if (d == 0) __stcg(to + GT * D + hl * 4, lse2);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        v.x += w[k] * p[k].x; v.y += w[k] * p[k].y; v.z += w[k] * p[k].z; v.w += w[k] * p[k].w;
       }
     }
-    if (!(begins && ends)) (begins ? open1 : open0) = first;
+    // (a run is its start's lane: the item's first segment, or lane 0 where it began before)
+    const float lse2 = head->run_lse[hl * 32 + (run.begins ? run.first : 0)];
+    if (run.begins && run.ends) {
+      finish(head->seg[run.first], hl, d, v, lse2);
+    } else {
+      float *to = a.parts + ((size_t)blockIdx.x * 2 + run.begins) * (PART / 4);
+      __stcg(reinterpret_cast<float4 *>(to + hl * D + d), v);
+      if (d == 0) __stcg(to + GT * D + hl * 4, lse2);
+    }
   }
-  if (open0 < 0 && open1 < 0) return;
 
   // Items that span CTAs: the last CTA to arrive joins their records.  The
   // counter is that of the CTA in which the item begins.
   __syncthreads();
   if (tid == 0) {
-    __threadfence();
+    int any = 0;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int e = k ? open1 : open0;
+      const AttnRun run = head->run[k ? max(runs - 1, 0) : 0];
+      const bool spans = runs > 0 && !(run.begins && run.ends) && run.begins == k;
       int last = 0;
-      if (e >= 0) {
-        const AttnSeg sg = head->seg[e];
-        const int c0 = attn_cta_of(sg.start, total, ctas), c1 = attn_cta_of(sg.start + sg.nu - 1, total, ctas);
+      if (spans) {
+        const AttnSeg sg = head->seg[run.first];
+        const int c0 = line.part_of(sg.start), n = line.part_of(sg.start + sg.nu - 1) - c0 + 1;
         s_from[k] = c0;
-        s_from[2 + k] = c1 - c0 + 1;
-        if (atomicAdd(&a.counters[c0], 1) == c1 - c0) {
+        s_from[2 + k] = n;
+        s_from[4 + k] = run.first;
+        if (!any) __threadfence();
+        any = 1;
+        if (atomicAdd(&a.counters[c0], 1) == n - 1) {
           a.counters[c0] = 0;
           last = 1;
         }
       }
       s_last[k] = last;
     }
-    __threadfence();
+    if (any) __threadfence();
   }
   __syncthreads();
   for (int k = 0; k < 2; ++k) {
     if (!s_last[k]) continue;
-    const AttnSeg sg = head->seg[k ? open1 : open0];
+    const AttnSeg sg = head->seg[s_from[4 + k]];
     const int n = s_from[2 + k];
     // the records: that of the CTA in which the item begins, then the others'
     const float *recs = a.parts + (size_t)s_from[k] * 2 * (PART / 4);
-    auto rec = [&](int c) { return recs + ((size_t)c * 2 + (c == 0 ? 1 : 0)) * (PART / 4); };
-    float *w = reinterpret_cast<float *>(smem + ATTN_HEAD);  // [n][GT], where the rings were
-    for (int i = tid; i < GT * n; i += THREADS) w[i] = __ldcg(rec(i / GT) + GT * D + i % GT * 4);
-    __syncthreads();
-    for (int hl = warp; hl < GT; hl += W + P) {
-      float m = -INFINITY, s = 0.f;
-      for (int c = lane; c < n; c += 32) m = fmaxf(m, w[c * GT + hl]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float r = m == -INFINITY ? 0.f : m;
-      for (int c = lane; c < n; c += 32) s += ex2(w[c * GT + hl] - r);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      const float inv = s == 0.f ? 0.f : 1.f / s;
-      for (int c = lane; c < n; c += 32) w[c * GT + hl] = ex2(w[c * GT + hl] - r) * inv;
-      if (lane == 0) s_lse[hl] = s == 0.f ? -INFINITY : r + lg2(s);
-    }
-    __syncthreads();
-    for (int x = tid; x < GT * D / 4; x += THREADS) {
+    for (int x = tid; x < QUADS; x += THREADS) {
       const int hl = x / (D / 4), d = (x % (D / 4)) * 4;
+      float m = -INFINITY, s = 0.f;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 16
-      for (int c = 0; c < n; ++c) {
-        const float wc = w[c * GT + hl];
-        const float4 p = __ldcg(reinterpret_cast<const float4 *>(rec(c) + hl * D + d));
-        v.x += wc * p.x; v.y += wc * p.y; v.z += wc * p.z; v.w += wc * p.w;
+      constexpr int AHEAD = 8;  // records on their way at a time, under a running reference
+      for (int c0 = 0; c0 < n; c0 += AHEAD) {
+        float ls[AHEAD], top = m;
+        float4 p[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+          const int c = min(c0 + j, n - 1);
+          const float *rec = recs + ((size_t)c * 2 + (c == 0 ? 1 : 0)) * (PART / 4);
+          ls[j] = __ldcg(rec + GT * D + hl * 4);
+          p[j] = __ldcg(reinterpret_cast<const float4 *>(rec + hl * D + d));
+        }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+          if (c0 + j >= n) ls[j] = -INFINITY;
+          top = fmaxf(top, ls[j]);
+        }
+        const float r = top == -INFINITY ? 0.f : top, keep = ex2(m - r);
+        m = top;
+        s *= keep;
+        v.x *= keep; v.y *= keep; v.z *= keep; v.w *= keep;
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+          if (c0 + j >= n) break;
+          const float w = ex2(ls[j] - r);
+          s += w;
+          v.x += w * p[j].x; v.y += w * p[j].y; v.z += w * p[j].z; v.w += w * p[j].w;
+        }
       }
-      finish(sg, hl, d, v, s_lse[hl]);
+      const float inv = s == 0.f ? 0.f : 1.f / s, lse2 = s == 0.f ? -INFINITY : m + lg2(s);
+      v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
+      finish(sg, hl, d, v, lse2);
     }
-    __syncthreads();
   }
 }
 
