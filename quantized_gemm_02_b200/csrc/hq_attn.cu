@@ -867,33 +867,49 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
   // the workspace: record [0] of an item begun before this CTA (the first run),
   // [1] of one that goes on after it (the last).
   constexpr int QUADS = GT * D / 4;
-  for (int i = tid; i < runs * QUADS; i += THREADS) {
-    const int rn = i / QUADS, x = i - rn * QUADS, hl = x / (D / 4), d = (x % (D / 4)) * 4;
-    const AttnRun run = head->run[rn];
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (unsigned mm = run.members; mm;) {
-      float w[2];
-      float4 p[2];
+  // Each thread has the first two records of FOUR quads on their way at a time.
+  constexpr int FOUR = 4;
+  for (int i0 = tid; i0 < runs * QUADS; i0 += FOUR * THREADS) {
+    float4 p[FOUR][2];
+    float w[FOUR][2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int e = mm ? __ffs(mm) - 1 : run.first;
-        w[k] = mm ? head->weight[hl * 32 + e] : 0.f;
-        p[k] = *reinterpret_cast<const float4 *>(record(e) + hl * D + d);
-        mm &= mm - 1;
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        v.x += w[k] * p[k].x; v.y += w[k] * p[k].y; v.z += w[k] * p[k].z; v.w += w[k] * p[k].w;
-      }
+    for (int u = 0; u < FOUR; ++u) {
+      const int i = i0 + u * THREADS, rn = i / QUADS, x = i - rn * QUADS, hl = x / (D / 4), d = (x % (D / 4)) * 4;
+      if (i >= runs * QUADS) break;
+      const unsigned mm = head->run[rn].members;
+      const int e0 = __ffs(mm) - 1, e1 = __ffs(mm & (mm - 1)) - 1;
+      w[u][0] = head->weight[hl * 32 + e0];
+      w[u][1] = e1 < 0 ? 0.f : head->weight[hl * 32 + e1];
+      p[u][0] = *reinterpret_cast<const float4 *>(record(e0) + hl * D + d);
+      p[u][1] = e1 < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4 *>(record(e1) + hl * D + d);
     }
-    // (a run is its start's lane: the item's first segment, or lane 0 where it began before)
-    const float lse2 = head->run_lse[hl * 32 + (run.begins ? run.first : 0)];
-    if (run.begins && run.ends) {
-      finish(head->seg[run.first], hl, d, v, lse2);
-    } else {
-      float *to = a.parts + ((size_t)blockIdx.x * 2 + run.begins) * (PART / 4);
-      __stcg(reinterpret_cast<float4 *>(to + hl * D + d), v);
-      if (d == 0) __stcg(to + GT * D + hl * 4, lse2);
+#pragma unroll
+    for (int u = 0; u < FOUR; ++u) {
+      const int i = i0 + u * THREADS, rn = i / QUADS, x = i - rn * QUADS, hl = x / (D / 4), d = (x % (D / 4)) * 4;
+      if (i >= runs * QUADS) break;
+      const AttnRun run = head->run[rn];
+      float4 v;
+      v.x = w[u][0] * p[u][0].x + w[u][1] * p[u][1].x;
+      v.y = w[u][0] * p[u][0].y + w[u][1] * p[u][1].y;
+      v.z = w[u][0] * p[u][0].z + w[u][1] * p[u][1].z;
+      v.w = w[u][0] * p[u][0].w + w[u][1] * p[u][1].w;
+      unsigned mm = run.members & (run.members - 1);
+#pragma unroll 2
+      for (mm &= mm - 1; mm; mm &= mm - 1) {
+        const int e = __ffs(mm) - 1;
+        const float we = head->weight[hl * 32 + e];
+        const float4 pe = *reinterpret_cast<const float4 *>(record(e) + hl * D + d);
+        v.x += we * pe.x; v.y += we * pe.y; v.z += we * pe.z; v.w += we * pe.w;
+      }
+      // (a run is its start's lane: the item's first segment, or lane 0 where it began before)
+      const float lse2 = head->run_lse[hl * 32 + (run.begins ? run.first : 0)];
+      if (run.begins && run.ends) {
+        finish(head->seg[run.first], hl, d, v, lse2);
+      } else {
+        float *to = a.parts + ((size_t)blockIdx.x * 2 + run.begins) * (PART / 4);
+        __stcg(reinterpret_cast<float4 *>(to + hl * D + d), v);
+        if (d == 0) __stcg(to + GT * D + hl * 4, lse2);
+      }
     }
   }
 
@@ -931,41 +947,57 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
     const int n = s_from[2 + k];
     // the records: that of the CTA in which the item begins, then the others'
     const float *recs = a.parts + (size_t)s_from[k] * 2 * (PART / 4);
-    for (int x = tid; x < QUADS; x += THREADS) {
-      const int hl = x / (D / 4), d = (x % (D / 4)) * 4;
-      float m = -INFINITY, s = 0.f;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      constexpr int AHEAD = 8;  // records on their way at a time, under a running reference
-      for (int c0 = 0; c0 < n; c0 += AHEAD) {
-        float ls[AHEAD], top = m;
-        float4 p[AHEAD];
+    // Records come from the L2 that another SM wrote, thousands of cycles away:
+    // sixteen pieces at a time are on their way, of as many quads as a thread has.
+    constexpr int MINE = QUADS > THREADS ? (QUADS + THREADS - 1) / THREADS : 1, AHEAD = 16 / MINE;
+    float m[MINE], s[MINE];
+    float4 v[MINE];
+#pragma unroll
+    for (int u = 0; u < MINE; ++u) {
+      m[u] = -INFINITY;
+      s[u] = 0.f;
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    auto quad = [&](int u) { return min(tid + u * THREADS, QUADS - 1); };
+    for (int c0 = 0; c0 < n; c0 += AHEAD) {  // under a running reference
+      float ls[MINE][AHEAD];
+      float4 p[MINE][AHEAD];
+#pragma unroll
+      for (int u = 0; u < MINE; ++u)
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
-          const int c = min(c0 + j, n - 1);
+          const int x = quad(u), c = c0 + j;
           const float *rec = recs + ((size_t)c * 2 + (c == 0 ? 1 : 0)) * (PART / 4);
-          ls[j] = __ldcg(rec + GT * D + hl * 4);
-          p[j] = __ldcg(reinterpret_cast<const float4 *>(rec + hl * D + d));
+          ls[u][j] = -INFINITY;
+          p[u][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (c < n) {
+            ls[u][j] = __ldcg(rec + GT * D + x / (D / 4) * 4);
+            p[u][j] = __ldcg(reinterpret_cast<const float4 *>(rec + x * 4));
+          }
         }
 #pragma unroll
-        for (int j = 0; j < AHEAD; ++j) {
-          if (c0 + j >= n) ls[j] = -INFINITY;
-          top = fmaxf(top, ls[j]);
-        }
-        const float r = top == -INFINITY ? 0.f : top, keep = ex2(m - r);
-        m = top;
-        s *= keep;
-        v.x *= keep; v.y *= keep; v.z *= keep; v.w *= keep;
+      for (int u = 0; u < MINE; ++u) {
+        float top = m[u];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) top = fmaxf(top, ls[u][j]);
+        const float r = top == -INFINITY ? 0.f : top, keep = ex2(m[u] - r);
+        m[u] = top;
+        s[u] *= keep;
+        v[u].x *= keep; v[u].y *= keep; v[u].z *= keep; v[u].w *= keep;
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
-          if (c0 + j >= n) break;
-          const float w = ex2(ls[j] - r);
-          s += w;
-          v.x += w * p[j].x; v.y += w * p[j].y; v.z += w * p[j].z; v.w += w * p[j].w;
+          const float w = ex2(ls[u][j] - r);
+          s[u] += w;
+          v[u].x += w * p[u][j].x; v[u].y += w * p[u][j].y; v[u].z += w * p[u][j].z; v[u].w += w * p[u][j].w;
         }
       }
-      const float inv = s == 0.f ? 0.f : 1.f / s, lse2 = s == 0.f ? -INFINITY : m + lg2(s);
-      v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
-      finish(sg, hl, d, v, lse2);
+    }
+#pragma unroll
+    for (int u = 0; u < MINE; ++u) {
+      const int x = tid + u * THREADS;
+      if (x >= QUADS) break;
+      const float inv = s[u] == 0.f ? 0.f : 1.f / s[u], lse2 = s[u] == 0.f ? -INFINITY : m[u] + lg2(s[u]);
+      finish(sg, x / (D / 4), (x % (D / 4)) * 4, make_float4(v[u].x * inv, v[u].y * inv, v[u].z * inv, v[u].w * inv), lse2);
     }
   }
 }
