@@ -59,39 +59,58 @@ __device__ __forceinline__ void sincos_small(float r, float &s, float &c) {
 
 // table[p] = amplitude * (cos(p f_0) .. cos(p f_{R/2-1}), sin(p f_0) ..).  The
 // angle of a far position does not fit fp32 (position 131072 leaves 2^-7 of a
-// radian there), so the product and the reduction are 64-bit: the angle is
-// counted in turns and brought to [-1/8, 1/8] of one; what is left goes
-// through fp32 sums, an error of about one fp32 step.  Bound by its stores:
-// 131072 x 128 (67 MB) in TABLE_LONG us of a floor of 10 (library sine and
-// cosine, two warps a block: 32).
+// radian there).  It is counted in turns, as a 64-bit binary fraction per
+// position (2^-53 of the frequency, 2^-64 of a turn), whose product with p
+// drops whole turns by itself; the upper 32 bits (2^-32 of a turn, 1.5e-9)
+// are brought to [-1/8, 1/8] of a turn and go through fp32 sums, an error of
+// about one fp32 step.  Bound by its stores: 131072 x 128 (67 MB) in TABLE_LONG us of
+// a floor of 10 (64-bit floating point in the loop: 21).
 constexpr int TABLE_THREADS = 256;
-__global__ void __launch_bounds__(TABLE_THREADS) rope_table_kernel(hq_rope_desc d, long long P, float *__restrict__ table) {
-  __shared__ double per[512];  // turns per position
+template <int V>
+__global__ void __launch_bounds__(TABLE_THREADS) rope_table_kernel(hq_rope_desc d, int P, float *__restrict__ table) {
+  __shared__ unsigned long long per[512];  // turns per position, times 2^64
   const int half = d.rot_dim / 2;
   const float amp = (float)d.amplitude;
-  for (int i = threadIdx.x; i < half; i += TABLE_THREADS) per[i] = rope_freq(d, i) / 6.283185307179586476925;
+  for (int i = threadIdx.x; i < half; i += TABLE_THREADS) {
+    const double turns = rope_freq(d, i) / 6.283185307179586476925;
+    per[i] = (unsigned long long)((turns - floor(turns)) * 18446744073709551616.0);
+  }
   __syncthreads();
-  // threads of a block: `cols` frequencies (all, up to the block's width) x rows
-  const int cols = min(half, TABLE_THREADS), rows = TABLE_THREADS / cols;
+  // Threads of a block: `cols` sets of V neighbouring frequencies (all, up to
+  // the block's width) x rows.
+  const int sets = half / V, cols = min(sets, TABLE_THREADS), rows = TABLE_THREADS / cols;
   const int row = threadIdx.x / cols;
   if (row >= rows) return;
-  for (int i = threadIdx.x - row * cols; i < half; i += cols) {
-    const double f = per[i];
-    const long long step = (long long)gridDim.x * rows;
-#pragma unroll 4
-    for (long long p = blockIdx.x * (long long)rows + row; p < P; p += step) {
-      const double turns = (double)p * f;
-      const double quarters = rint(turns * 4.0);
-      const float r = (float)((turns - quarters * 0.25) * 6.283185307179586476925);
-      const int quad = (int)((long long)quarters & 3);
-      float s, c;
-      sincos_small(r, s, c);
-      float co = (quad & 1) ? s : c, si = (quad & 1) ? c : s;
-      if (quad == 1 || quad == 2) co = -co;
-      if (quad >= 2) si = -si;
-      float *to = table + p * d.rot_dim + i;
-      to[0] = amp * co;
-      to[half] = amp * si;
+  for (int i = (threadIdx.x - row * cols); i < sets; i += cols) {
+    uint32_t lo[V], hi[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      lo[j] = (uint32_t)per[i * V + j];
+      hi[j] = (uint32_t)(per[i * V + j] >> 32);
+    }
+    const unsigned step = gridDim.x * rows;
+    float *to = table + (size_t)(blockIdx.x * rows + row) * d.rot_dim + i * V;
+    for (unsigned p = blockIdx.x * rows + row; p < (unsigned)P; p += step, to += (size_t)step * d.rot_dim) {
+      float co[V], si[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const uint32_t turn = __umulhi(p, lo[j]) + p * hi[j];  // of 2^32
+        const uint32_t quad = (turn + (1u << 29)) >> 30;
+        const float r = (float)(int)(turn - (quad << 30)) * (6.283185307179586f / 4294967296.f);
+        float s, c;
+        sincos_small(r, s, c);
+        co[j] = amp * ((quad & 1) ? s : c);
+        si[j] = amp * ((quad & 1) ? c : s);
+        if (quad == 1 || quad == 2) co[j] = -co[j];
+        if (quad & 2) si[j] = -si[j];
+      }
+      if constexpr (V == 4) {
+        __stcs(reinterpret_cast<float4 *>(to), make_float4(co[0], co[1], co[2], co[3]));
+        __stcs(reinterpret_cast<float4 *>(to + half), make_float4(si[0], si[1], si[2], si[3]));
+      } else {
+        to[0] = co[0];
+        to[half] = si[0];
+      }
     }
   }
 }
@@ -99,9 +118,11 @@ __global__ void __launch_bounds__(TABLE_THREADS) rope_table_kernel(hq_rope_desc 
 hq_status launch_rope_table(const hq_rope_desc *d, int P, float *table, cudaStream_t st) {
   hq_rope_desc r = *d;
   if (r.amplitude == 0.0) r.amplitude = 1.0;
-  const int half = r.rot_dim / 2, rows = TABLE_THREADS / (half < TABLE_THREADS ? half : TABLE_THREADS);
-  const int want = (P + rows - 1) / rows;
-  rope_table_kernel<<<want < 148 * 8 ? want : 148 * 8, TABLE_THREADS, 0, st>>>(r, P, table);
+  const int half = r.rot_dim / 2, v = half % 4 == 0 ? 4 : 1, sets = half / v;
+  const int rows = TABLE_THREADS / (sets < TABLE_THREADS ? sets : TABLE_THREADS);
+  const int want = (P + rows - 1) / rows, blocks = want < 148 * 8 ? want : 148 * 8;
+  if (v == 4) rope_table_kernel<4><<<blocks, TABLE_THREADS, 0, st>>>(r, P, table);
+  else rope_table_kernel<1><<<blocks, TABLE_THREADS, 0, st>>>(r, P, table);
   return check_launch();
 }
 
