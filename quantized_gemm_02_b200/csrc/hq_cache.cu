@@ -432,35 +432,36 @@ struct KvRows {
 // the row in the unit and move whole vectors (split where their octets are in
 // two units); other groups (a decoding step's tokens) go by the token and move
 // octet by octet.  No shared memory, no barrier.
-constexpr int KV_THREADS = 64;
+constexpr int KV_THREADS = 128;
 
 struct KvGroup {
   long long unit;  // lane i (and i + 16): byte offset of token i's unit (head 0), -1: none
-  int row;
+  int row, pos;    // and its position
   bool run;
   int r0;
 };
+struct KvToken {   // what a lane reads of its token
+  long long slot;
+  int pos;
+};
+__device__ __forceinline__ KvToken kv_token(const KvRows &w, const RopeArgs *rope, long long t0) {
+  const long long t = t0 + (threadIdx.x & 15);
+  return t < w.T ? KvToken{w.slots[t], rope ? rope->pos[t] : 0} : KvToken{-1, 0};
+}
 
 template <int FMT, int D>
-__device__ __forceinline__ KvGroup kv_group(const KvArgs &a, const KvRows &w, const RopeArgs *rope, long long t0) {
+__device__ __forceinline__ KvGroup kv_group(const KvArgs &a, const KvToken &k, const RopeArgs *rope) {
   const int i = threadIdx.x & 15;
-  const long long t = t0 + i;
-  KvGroup s{-1, 0, false, 0};
-  if (t < w.T) {
-    const long long slot = w.slots[t];
-    if (slot >= a.slots_total) set_device_error(HQ_ERR_DEVICE_INDEX);
-    if (slot >= 0 && slot < a.slots_total) {
-      const long long pg = slot >> 31 ? slot / a.page : (long long)((uint32_t)slot / (uint32_t)a.page);
-      const int off = (int)(slot - pg * a.page);
-      s.unit = (long long)((size_t)pg * a.page_bytes + (size_t)(off >> 4) * kv_unit_bytes(FMT, D));
-      s.row = off & 15;
-    }
-    if (rope && s.unit >= 0) {
-      const int p = rope->pos[t];
-      if (p < 0 || p >= rope->P) {
-        set_device_error(HQ_ERR_DEVICE_INDEX);
-        s.unit = -1;
-      }
+  KvGroup s{-1, 0, k.pos, false, 0};
+  if (k.slot >= a.slots_total) set_device_error(HQ_ERR_DEVICE_INDEX);
+  if (k.slot >= 0 && k.slot < a.slots_total) {
+    const long long pg = k.slot >> 31 ? k.slot / a.page : (long long)((uint32_t)k.slot / (uint32_t)a.page);
+    const int off = (int)(k.slot - pg * a.page);
+    s.unit = (long long)((size_t)pg * a.page_bytes + (size_t)(off >> 4) * kv_unit_bytes(FMT, D));
+    s.row = off & 15;
+    if (rope && (k.pos < 0 || k.pos >= rope->P)) {
+      set_device_error(HQ_ERR_DEVICE_INDEX);
+      s.unit = -1;
     }
   }
   const int r0 = __shfl_sync(0xffffffffu, s.row, 0);
@@ -571,8 +572,8 @@ __host__ __device__ constexpr int kv_parts(int fmt, int D) { return fmt == A_FP8
 
 // Bound by HBM: WRITE_NOTE
 template <int FMT, int D, bool ROPE>
-__global__ void __launch_bounds__(KV_THREADS, FMT == A_FP8 && ROPE ? 8 : 12)
-    kv_write_kernel(KvArgs a, KvRows w, RopeArgs rope, int kv_blocks) {
+__global__ void __launch_bounds__(KV_THREADS, FMT != A_FP8 ? 8 : ROPE ? 4 : 6)
+    kv_write_kernel(KvArgs a, KvRows w, RopeArgs rope, unsigned kv_blocks) {
   if (blockIdx.x >= kv_blocks) {  // these rotate the rope.H heads of q
     rope_rows(rope, blockIdx.x - kv_blocks);
     return;
@@ -580,14 +581,13 @@ __global__ void __launch_bounds__(KV_THREADS, FMT == A_FP8 && ROPE ? 8 : 12)
   constexpr int NB = D / 32, NQ = D / 64, CB = kv_code_bytes(FMT, D), SB = kv_scale_bytes(FMT, D), GS = kv_granule(FMT);
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   constexpr int PARTS = kv_parts(FMT, D);
-  const long long work = ((long long)w.T + 15) / 16 * a.H * 2 * PARTS, step = (long long)kv_blocks * (KV_THREADS / 32);
-  for (long long it = blockIdx.x * (KV_THREADS / 32) + (threadIdx.x >> 5); it < work; it += step) {
-    const int part = (int)(it % PARTS);
-    const bool is_v = it / PARTS & 1;
-    const long long ih = it / PARTS >> 1, grp = ih >> 31 ? ih / a.H : (long long)((uint32_t)ih / (uint32_t)a.H);
-    const int h = (int)(ih - grp * a.H);
-    const long long t0 = grp * 16;
-    const KvGroup s = kv_group<FMT, D>(a, w, ROPE ? &rope : nullptr, t0);
+  // the heads of a group are neighbours: they share the table's rows in L1
+  const long long it = blockIdx.x * (long long)(KV_THREADS / 32) + (threadIdx.x >> 5), sets = it >> 31 ? it / a.H : (long long)((uint32_t)it / (uint32_t)a.H);
+  const int h = (int)(it - sets * a.H), part = (int)((sets >> 1) % PARTS);
+  const bool is_v = sets & 1;
+  const long long t0 = (sets >> 1) / PARTS * 16;
+  if (t0 < w.T) {
+    const KvGroup s = kv_group<FMT, D>(a, kv_token(w, ROPE ? &rope : nullptr, t0), ROPE ? &rope : nullptr);
     uint8_t *base = a.pages + (size_t)h * a.page_units * kv_unit_bytes(FMT, D);
 
     if (!is_v) {
@@ -598,7 +598,8 @@ __global__ void __launch_bounds__(KV_THREADS, FMT == A_FP8 && ROPE ? 8 : 12)
       for (int k = 0; k < 2; ++k) {
         kr[k] = kv_row(s, g + 8 * k);
         x[k] = w.k + (t0 + kr[k].i) * w.ks + (size_t)h * D;
-        if (ROPE && kr[k].unit >= 0) tab[k] = rope.table + (size_t)rope.pos[t0 + kr[k].i] * rope.rot;
+        const int pos = __shfl_sync(0xffffffffu, s.pos, kr[k].i);
+        if (ROPE && kr[k].unit >= 0) tab[k] = rope.table + (size_t)pos * rope.rot;
       }
       auto key = [&](int k, int b, float *f) {  // octet 4 b + t of key k as fp32
         if (kr[k].unit < 0) {
@@ -698,7 +699,7 @@ __global__ void __launch_bounds__(KV_THREADS, FMT == A_FP8 && ROPE ? 8 : 12)
                 *reinterpret_cast<uint32_t *>(base + kr[k].unit + k_octet<GS>(4 * (b + j) + t, kr[k].row)) = c[j][k];
         }
       }
-      continue;
+      return;
     }
 
     KvRow vr[4];
@@ -848,7 +849,7 @@ __device__ __forceinline__ uint4 nvfp4_values(uint32_t w, uint32_t sb, float g) 
 
 // Bound by HBM: READ_NOTE
 template <int FMT, int D>
-__global__ void __launch_bounds__(KV_THREADS, 12) kv_read_kernel(KvArgs a, KvRows w) {
+__global__ void __launch_bounds__(KV_THREADS, 6) kv_read_kernel(KvArgs a, KvRows w) {
   constexpr int NB = D / 32, NQ = D / 64, CB = kv_code_bytes(FMT, D), SB = kv_scale_bytes(FMT, D), GS = kv_granule(FMT);
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const long long work = ((long long)w.T + 15) / 16 * a.H * 2, step = (long long)gridDim.x * (KV_THREADS / 32);
@@ -858,7 +859,7 @@ __global__ void __launch_bounds__(KV_THREADS, 12) kv_read_kernel(KvArgs a, KvRow
     const long long ih = it >> 1, grp = ih >> 31 ? ih / a.H : (long long)((uint32_t)ih / (uint32_t)a.H);
     const int h = (int)(ih - grp * a.H);
     const long long t0 = grp * 16;
-    const KvGroup s = kv_group<FMT, D>(a, w, nullptr, t0);
+    const KvGroup s = kv_group<FMT, D>(a, kv_token(w, nullptr, t0), nullptr);
     const uint8_t *base = a.pages + (size_t)h * a.page_units * kv_unit_bytes(FMT, D);
     // granule n of vector i: the octets of the lane's rows, whole or one by one
     if (!is_v) {
@@ -1012,28 +1013,24 @@ static hq_status kv_dispatch(int fmt, int D, F &&f) {
   return HQ_ERR_UNSUPPORTED;
 }
 
-// Blocks of two warps, no more than the SMs hold at a time.
-static int kv_blocks(long long warps) {
-  const long long blocks = (warps + KV_THREADS / 32 - 1) / (KV_THREADS / 32);
-  return (int)(blocks < 148 * 12 ? blocks : 148 * 12);
-}
+static long long kv_blocks(long long warps) { return (warps + KV_THREADS / 32 - 1) / (KV_THREADS / 32); }
 
 hq_status launch_kv_write(int fmt, int D, const KvArgs &a, const KvRows &w, const RopeArgs &rope, cudaStream_t st) {
   return kv_dispatch(fmt, D, [&](auto F, auto DD) {
-    const int kb = kv_blocks(((long long)w.T + 15) / 16 * a.H * 2 * kv_parts(F, DD));
+    const long long kb = kv_blocks(((long long)w.T + 15) / 16 * a.H * 2 * kv_parts(F, DD));
     if (rope.rot) {
       // A step's q is rotated by further blocks of the launch; a prompt's by
       // the rotation's own kernel, whose blocks are four times as many to an SM
       // (8191 x 16 heads x 256 beside the write: FUSED us against SPLIT).
       const long long qb = rope.H ? rope_blocks(rope) : 0;
       const bool split = qb > 148 * 4;
-      kv_write_kernel<F, DD, true><<<kb + (split ? 0 : (int)qb), KV_THREADS, 0, st>>>(a, w, rope, kb);
+      kv_write_kernel<F, DD, true><<<(unsigned)(kb + (split ? 0 : qb)), KV_THREADS, 0, st>>>(a, w, rope, (unsigned)kb);
       if (split) {
         const hq_status s = check_launch();
         return s != HQ_OK ? s : launch_rope(rope_resplit(rope, ROPE_THREADS), st);
       }
     } else {
-      kv_write_kernel<F, DD, false><<<kb, KV_THREADS, 0, st>>>(a, w, rope, kb);
+      kv_write_kernel<F, DD, false><<<(unsigned)kb, KV_THREADS, 0, st>>>(a, w, rope, (unsigned)kb);
     }
     return check_launch();
   });
@@ -1041,7 +1038,8 @@ hq_status launch_kv_write(int fmt, int D, const KvArgs &a, const KvRows &w, cons
 
 hq_status launch_kv_read(int fmt, int D, const KvArgs &a, const KvRows &w, cudaStream_t st) {
   return kv_dispatch(fmt, D, [&](auto F, auto DD) {
-    kv_read_kernel<F, DD><<<kv_blocks(((long long)w.T + 15) / 16 * a.H * 2), KV_THREADS, 0, st>>>(a, w);
+    const long long kb = kv_blocks(((long long)w.T + 15) / 16 * a.H * 2);
+    kv_read_kernel<F, DD><<<(unsigned)(kb < 148 * 6 ? kb : 148 * 6), KV_THREADS, 0, st>>>(a, w);
     return check_launch();
   });
 }
