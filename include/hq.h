@@ -159,8 +159,8 @@ typedef struct {
 HQ_API const char *hq_status_string(hq_status s);
 
 /* Reads and clears the current device's device-side error word after
- * synchronising `stream`.  Returns HQ_OK, HQ_ERR_TIMEOUT or
- * HQ_ERR_DEVICE_INDEX. */
+ * synchronising `stream`.  Returns HQ_OK, HQ_ERR_TIMEOUT,
+ * HQ_ERR_DEVICE_INDEX or (hq_paged_attn) HQ_ERR_UNSUPPORTED. */
 HQ_API hq_status hq_device_error(hq_stream_t stream);
 
 /* Diagnostics (no counterpart in the pages): launches one warp that waits
@@ -449,8 +449,11 @@ HQ_API hq_status hq_gemm_noalloc(const hq_quant_desc *desc, int M, int N, int K,
  * with hq_quant_act's recipes, and one new token per sequence attends over
  * it.  All tensors are bf16 with unit stride along the channels; strides
  * between tokens (and heads, where given) are in elements, non-negative and
- * multiples of 8, so that q, k and v may be parts of one projection's output.
- * Pointers and the stream belong to the current device.
+ * multiples of 8, so that q, k and v may be parts of one projection's output;
+ * rows of an output must not overlap.  Index arrays, lse and global_scale need
+ * their own type's alignment only, the others 16 bytes.  Pointers and the
+ * stream belong to the current device.  Tokens times heads of a call stay
+ * below 2^31.
  * ---------------------------------------------------------------------- */
 
 /* How the frequencies of a rotation are scaled for contexts longer than the
@@ -489,7 +492,8 @@ HQ_API hq_status hq_rope_table(const hq_rope_desc *rope, int P, float *table, hq
  * (device int32 [T], values in [0, P)) of `table`, each pair (a, b) becomes
  * (a c - b s, b c + a s), every step an fp32 operation, rounded to bf16 at the
  * end; channels from rot_dim on are copied.  out may be x with the same
- * strides; other overlaps are not allowed.  D a multiple of 8, at most 1024.
+ * strides; other overlaps are not allowed.  D a multiple of 8, at most 1024;
+ * H at most 65536.
  * A position outside [0, P) sets HQ_ERR_DEVICE_INDEX in the device error word
  * and leaves the token's out row as it was.  (The inverse rotation, which is
  * also the gradient, takes a table with the sines negated.) */
@@ -560,12 +564,16 @@ HQ_API hq_status hq_kv_read(const hq_kv_desc *kv, int T, const int64_t *slots, c
  *   out[b, i] = sum_j exp(x_j) v_j / sum_j exp(x_j)   bf16 [B, q_heads, head_dim]
  *   lse[b, i] = ln sum_j exp(x_j)                     fp32 [B, q_heads], may be NULL
  * A length of 0 gives out = 0 and lse = -inf.  A length below 0 or above
- * max_pages * page_size sets HQ_ERR_DEVICE_INDEX and counts as 0 or as that
- * bound; a page id outside the cache sets it too and its tokens are left out.
- * Slots past a length may hold anything.  Scores, softmax and sums are fp32;
- * the result does not depend on timing.  `workspace` as for hq_gemm: of
+ * max_pages * page_size (at most 2^30) sets HQ_ERR_DEVICE_INDEX and counts as
+ * 0 or as that bound; a page id outside the cache sets it too and its tokens
+ * are left out.  Slots past a length and pages before the window may hold
+ * anything.  Scores, softmax and sums are fp32; the result does not depend on
+ * timing.  From 2^34 tokens times kv heads on (each once per 16 query heads) a
+ * call may set HQ_ERR_UNSUPPORTED in the device error word and then writes
+ * nothing but the rows of empty sequences.  `workspace` as for hq_gemm: of
  * hq_paged_attn_workspace_bytes() bytes, its counters zero when first used and
- * left zero by every completed call; calls that share one must be ordered. */
+ * left zero by every completed call (after HQ_ERR_TIMEOUT, zero them again);
+ * calls that share one must be ordered. */
 HQ_API size_t hq_paged_attn_workspace_bytes(const hq_kv_desc *kv, int B, int q_heads);
 HQ_API hq_status hq_paged_attn(const hq_kv_desc *kv, int B, int q_heads, const void *q_bf16, int64_t q_stride,
                                const float *global_scale, int num_pages, const void *pages,

@@ -708,9 +708,16 @@ static bool valid_rope(const hq_rope_desc *r, int D) {
   return r->rot_dim >= 2 && r->rot_dim <= D && (r->rot_dim % 2) == 0 && (r->interleaved == 0 || r->interleaved == 1);
 }
 
-// A stride between rows of `width` elements: 16-byte steps that do not overlap
-// (0 rows or one row: any).
-static bool valid_stride(int64_t stride) { return stride >= 0 && (stride % 8) == 0; }
+// Strides between rows, elements: 16-byte steps; input rows may overlap (a
+// stride of 0 repeats one), `rows` output rows of `width` may not.
+static bool valid_stride(int64_t stride) { return stride >= 0 && stride <= (1ll << 40) && (stride % 8) == 0; }
+static bool valid_out_stride(int64_t stride, int64_t rows, int64_t width) {
+  return valid_stride(stride) && (rows <= 1 || stride >= width);
+}
+// Index arrays and fp32 values need their own alignment only.
+static bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+// Launch grids are limited to 2^31 - 1 blocks; no tensor in memory comes near.
+static bool valid_work(int64_t T, int64_t heads) { return T * heads < (1ll << 31); }
 
 static hq_status check_kv(const hq_kv_desc *kv, int *fmt) {
   if (!kv) return HQ_ERR_INVALID_ARG;
@@ -724,7 +731,7 @@ static hq_status check_kv(const hq_kv_desc *kv, int *fmt) {
 // The cache's pointers, shared by every call on it.
 static hq_status check_pages(const hq_kv_desc *kv, int num_pages, const void *pages, const float *global_scale) {
   if (num_pages < 1 || !pages || !aligned16(pages)) return HQ_ERR_INVALID_ARG;
-  return (kv->dtype == HQ_NVFP4) == (global_scale != nullptr) ? HQ_OK : HQ_ERR_INVALID_ARG;
+  return (kv->dtype == HQ_NVFP4) == (global_scale != nullptr) && aligned_to(global_scale, 4) ? HQ_OK : HQ_ERR_INVALID_ARG;
 }
 
 hq_status hq_rope_table(const hq_rope_desc *rope, int P, float *table, hq_stream_t stream) {
@@ -743,14 +750,19 @@ hq_status hq_rope_table(const hq_rope_desc *rope, int P, float *table, hq_stream
 hq_status hq_rope(const hq_rope_desc *rope, int T, int H, int D, const void *x_bf16, int64_t x_token_stride,
                   int64_t x_head_stride, const int32_t *positions, const float *table, int P, void *out_bf16,
                   int64_t out_token_stride, int64_t out_head_stride, hq_stream_t stream) {
-  if (!rope || T < 0 || H < 1 || D < 8 || D > 1024 || (D % 8) != 0 || !valid_rope(rope, D) || P < 1)
+  if (!rope || T < 0 || H < 1 || H > 65536 || !valid_work(T, H) || D < 8 || D > 1024 || (D % 8) != 0 || !valid_rope(rope, D) || P < 1)
     return HQ_ERR_INVALID_ARG;
-  if (!valid_stride(x_token_stride) || !valid_stride(x_head_stride) || !valid_stride(out_token_stride) ||
-      !valid_stride(out_head_stride))
+  if (!valid_stride(x_token_stride) || !valid_stride(x_head_stride) || !valid_out_stride(out_token_stride, T, D) ||
+      !valid_out_stride(out_head_stride, H, D))
     return HQ_ERR_INVALID_ARG;
   if (T == 0) return HQ_OK;
+  // heads within tokens, or tokens within heads
+  if (T > 1 && H > 1 && out_token_stride < (int64_t)(H - 1) * out_head_stride + D &&
+      out_head_stride < (int64_t)(T - 1) * out_token_stride + D)
+    return HQ_ERR_INVALID_ARG;
   if (!x_bf16 || !positions || !table || !out_bf16 || !aligned16(x_bf16) || !aligned16(table) || !aligned16(out_bf16))
     return HQ_ERR_INVALID_ARG;
+  if (!aligned_to(positions, 4)) return HQ_ERR_INVALID_ARG;
   if (x_bf16 == out_bf16 && (x_token_stride != out_token_stride || x_head_stride != out_head_stride))
     return HQ_ERR_INVALID_ARG;
   if (!device_is_sm100()) return HQ_ERR_ARCH;
@@ -772,14 +784,16 @@ static hq_status kv_write(const hq_rope_desc *rope, const hq_kv_desc *kv, int T,
   int fmt;
   const hq_status s = check_kv(kv, &fmt);
   if (s != HQ_OK) return s;
-  if (T < 0 || !valid_stride(k_stride) || !valid_stride(v_stride)) return HQ_ERR_INVALID_ARG;
+  if (T < 0 || !valid_work(T, kv->heads) || !valid_stride(k_stride) || !valid_stride(v_stride)) return HQ_ERR_INVALID_ARG;
   if (rope) {
-    if (!valid_rope(rope, kv->head_dim) || P < 1 || q_heads < 0 || q_heads > 65536) return HQ_ERR_INVALID_ARG;
-    if (q_heads && (!valid_stride(q_stride) || !valid_stride(q_out_stride))) return HQ_ERR_INVALID_ARG;
+    if (!valid_rope(rope, kv->head_dim) || P < 1 || q_heads < 0 || q_heads > 65536 || !valid_work(T, q_heads))
+      return HQ_ERR_INVALID_ARG;
+    if (q_heads && (!valid_stride(q_stride) || !valid_out_stride(q_out_stride, T, (int64_t)q_heads * kv->head_dim)))
+      return HQ_ERR_INVALID_ARG;
   }
   if (T == 0) return HQ_OK;
-  if (!k || !v || !slots || !aligned16(k) || !aligned16(v)) return HQ_ERR_INVALID_ARG;
-  if (rope && (!positions || !table || !aligned16(table))) return HQ_ERR_INVALID_ARG;
+  if (!k || !v || !slots || !aligned16(k) || !aligned16(v) || !aligned_to(slots, 8)) return HQ_ERR_INVALID_ARG;
+  if (rope && (!positions || !aligned_to(positions, 4) || !table || !aligned16(table))) return HQ_ERR_INVALID_ARG;
   if (q_heads ? (!q || !q_out || !aligned16(q) || !aligned16(q_out) || (q == q_out && q_stride != q_out_stride))
               : (q || q_out))
     return HQ_ERR_INVALID_ARG;
@@ -824,9 +838,12 @@ hq_status hq_kv_read(const hq_kv_desc *kv, int T, const int64_t *slots, const fl
   int fmt;
   const hq_status s = check_kv(kv, &fmt);
   if (s != HQ_OK) return s;
-  if (T < 0 || !valid_stride(k_stride) || !valid_stride(v_stride)) return HQ_ERR_INVALID_ARG;
+  const int64_t width = (int64_t)kv->heads * kv->head_dim;
+  if (T < 0 || !valid_work(T, kv->heads) || (k_out_bf16 && !valid_out_stride(k_stride, T, width)) ||
+      (v_out_bf16 && !valid_out_stride(v_stride, T, width)))
+    return HQ_ERR_INVALID_ARG;
   if (T == 0) return HQ_OK;
-  if (!slots || (!k_out_bf16 && !v_out_bf16) || !aligned16(k_out_bf16) || !aligned16(v_out_bf16))
+  if (!slots || !aligned_to(slots, 8) || (!k_out_bf16 && !v_out_bf16) || !aligned16(k_out_bf16) || !aligned16(v_out_bf16))
     return HQ_ERR_INVALID_ARG;
   const hq_status ps = check_pages(kv, num_pages, pages, global_scale);
   if (ps != HQ_OK) return ps;
@@ -862,12 +879,14 @@ hq_status hq_paged_attn(const hq_kv_desc *kv, int B, int q_heads, const void *q_
   int fmt;
   const hq_status s = check_kv(kv, &fmt);
   if (s != HQ_OK) return s;
-  if (!valid_q_heads(kv, B, q_heads) || !valid_stride(q_stride) || !valid_stride(out_stride) || max_pages < 1 ||
-      (int64_t)max_pages * kv->page_size > INT32_MAX || window < 0)
+  if (!valid_q_heads(kv, B, q_heads) || !valid_stride(q_stride) ||
+      !valid_out_stride(out_stride, B, (int64_t)q_heads * kv->head_dim) || max_pages < 1 ||
+      (int64_t)max_pages * kv->page_size > (1 << 30) || window < 0)
     return HQ_ERR_INVALID_ARG;
   if (!(scale >= -3e38f && scale <= 3e38f)) return HQ_ERR_INVALID_ARG;
   if (B == 0) return HQ_OK;
-  if (!q_bf16 || !page_table || !lengths || !out_bf16 || !aligned16(q_bf16) || !aligned16(out_bf16))
+  if (!q_bf16 || !page_table || !lengths || !out_bf16 || !aligned16(q_bf16) || !aligned16(out_bf16) ||
+      !aligned_to(page_table, 4) || !aligned_to(lengths, 4) || !aligned_to(lse, 4))
     return HQ_ERR_INVALID_ARG;
   const hq_status ps = check_pages(kv, num_pages, pages, global_scale);
   if (ps != HQ_OK) return ps;

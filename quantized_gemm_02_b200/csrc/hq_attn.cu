@@ -63,7 +63,7 @@ struct AttnArgs {
 // The tokens a sequence's query sees: [first, len).
 __device__ __forceinline__ int attn_range(const AttnArgs &a, int b, int &first) {
   int n = a.lengths[b];
-  const int most = a.max_pages * a.kv.page;
+  const int most = a.max_pages * a.kv.page;  // at most 2^30
   if (n < 0 || n > most) {
     set_device_error(HQ_ERR_DEVICE_INDEX);
     n = n < 0 ? 0 : most;

@@ -70,22 +70,32 @@ def test_rope_arguments():
     for bad in (dict(T=-1), dict(H=0), dict(D=60), dict(D=1032), dict(D=0), dict(x=24), dict(x=None), dict(pos=None), dict(table=None),
                 dict(table=20), dict(P=0), dict(out=None), dict(out=40), dict(xt=127), dict(xh=-64), dict(ot=4), dict(oh=12),
                 dict(rope=hq.RopeDesc(rot_dim=66)), dict(rope=hq.RopeDesc(rot_dim=7)), dict(rope=hq.RopeDesc(rot_dim=64, interleaved=3)),
-                dict(out=16, ot=256)):
+                dict(out=16, ot=256), dict(ot=64), dict(oh=0), dict(oh=32), dict(ot=0, oh=128), dict(pos=18), dict(H=65537),
+                dict(T=1 << 30, H=4)):
         with pytest.raises(hq.HQError) as e:
             call(**bad)
         assert e.value.status == 1, bad
     call(T=0, x=None, out=None)
 
 
+def test_rope_output_layouts_that_do_not_overlap():
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("would run")
+    for strides in ((128, 64), (64, 128), (64, 4096)):  # heads within tokens, tokens within heads
+        refused(7, hq.hq_rope, hq.RopeDesc(rot_dim=64), 2, 2, 64, 16, 0, 0, 16, 16, 8, 1 << 20, *strides)
+
+
 def test_write_and_read_arguments():
     w = lambda d=OK, T=1, k=16, ks=1024, v=16, vs=1024, slots=16, g=None, n=4, pages=16: (d, T, k, ks, v, vs, slots, g, n, pages)  # noqa: E731
     for bad in (dict(T=-1), dict(k=None), dict(v=None), dict(k=8), dict(v=24), dict(ks=1020), dict(vs=-8), dict(slots=None), dict(n=0),
-                dict(pages=None), dict(pages=8), dict(g=16), dict(d=kv(dtype=hq.HQ_NVFP4))):
+                dict(slots=20), dict(T=1 << 29), dict(pages=None), dict(pages=8), dict(g=16), dict(d=kv(dtype=hq.HQ_NVFP4)),
+                dict(d=kv(dtype=hq.HQ_NVFP4), g=18)):
         refused(1, hq.hq_kv_write, *w(**bad))
     hq.hq_kv_write(*w(T=0, k=None, v=None, slots=None, pages=None), stream=0)
     r = lambda d=OK, T=1, slots=16, g=None, n=4, pages=16, k=16, ks=1024, v=16, vs=1024: (d, T, slots, g, n, pages, k, ks, v, vs)  # noqa: E731
     for bad in (dict(T=-1), dict(slots=None), dict(k=None, v=None), dict(k=8), dict(v=8), dict(ks=4), dict(vs=-8), dict(n=0),
-                dict(pages=None), dict(g=16), dict(d=kv(dtype=hq.HQ_NVFP4))):
+                dict(slots=12), dict(T=2, ks=1016), dict(T=2, vs=0), dict(pages=None), dict(g=16), dict(d=kv(dtype=hq.HQ_NVFP4))):
         refused(1, hq.hq_kv_read, *r(**bad))
     hq.hq_kv_read(*r(T=0, slots=None, pages=None, k=None, v=None), stream=0)
 
@@ -95,7 +105,7 @@ def test_rope_write_arguments():
     names = ["rope", "kv", "T", "Hq", "q", "qs", "qo", "qos", "k", "ks", "v", "vs", "pos", "table", "P", "slots", "g", "n", "pages"]
     good = dict(zip(names, [rope, OK, 1, 8, 16, 1024, 16, 1024, 16, 1024, 16, 1024, 16, 16, 4, 16, None, 4, 16]))
     for bad in (dict(rope=hq.RopeDesc(rot_dim=130)), dict(rope=hq.RopeDesc(rot_dim=0)), dict(Hq=-1), dict(q=None), dict(qo=None),
-                dict(q=8), dict(qs=4), dict(qos=-8), dict(qos=2048), dict(pos=None), dict(table=None), dict(table=20), dict(P=0),
+                dict(q=8), dict(qs=4), dict(qos=-8), dict(qos=2048), dict(qo=32, T=2, qos=512), dict(pos=17), dict(pos=None), dict(table=None), dict(table=20), dict(P=0),
                 dict(Hq=0), dict(k=None), dict(slots=None), dict(pages=None)):
         refused(1, hq.hq_rope_kv_write, *dict(good, **bad).values())
     hq.hq_rope_kv_write(*dict(good, T=0).values(), stream=0)
@@ -107,7 +117,7 @@ def test_attention_arguments():
     assert need > 0
     good = dict(zip(names, [OK, 4, 32, 16, 4096, None, 9, 16, 16, 7, 16, 0.1, 0, 16, 4096, None, 16, need]))
     for bad in (dict(B=-1), dict(B=1 << 21), dict(Hq=0), dict(Hq=4), dict(Hq=33), dict(q=None), dict(q=8), dict(qs=4), dict(g=16), dict(n=0),
-                dict(pages=None), dict(pages=8), dict(pt=None), dict(most=0), dict(most=1 << 28), dict(lens=None), dict(scale=float("nan")),
+                dict(pages=None), dict(pages=8), dict(pt=None), dict(most=0), dict(most=1 << 27), dict(pt=18), dict(lens=18), dict(lse=18), dict(os=2048), dict(os=0), dict(lens=None), dict(scale=float("nan")),
                 dict(scale=float("inf")), dict(window=-1), dict(out=None), dict(out=8), dict(os=-8), dict(os=12),
                 dict(kv=kv(dtype=hq.HQ_NVFP4))):
         refused(1, hq.hq_paged_attn, *dict(good, **bad).values())
@@ -121,3 +131,15 @@ def test_tensors_that_are_not_on_the_device_are_refused():
     import torch
     t = torch.zeros(4, 64)
     refused(1, hq.hq_rope_table, hq.RopeDesc(rot_dim=64, base=10000.0), 4, t)
+
+
+def test_index_tensors_of_another_width_are_refused():
+    import torch
+    i32, i64 = torch.zeros(4, dtype=torch.int32), torch.zeros(4, dtype=torch.int64)
+    refused(1, hq.hq_kv_write, OK, 1, 16, 1024, 16, 1024, i32, None, 4, 16)
+    refused(1, hq.hq_kv_read, OK, 1, i32, None, 4, 16, 16, 1024, 16, 1024)
+    refused(1, hq.hq_rope, hq.RopeDesc(rot_dim=64), 1, 1, 64, 16, 64, 64, i64, 16, 4, 32, 64, 64)
+    need = hq.hq_paged_attn_workspace_bytes(OK, 1, 8)
+    refused(1, hq.hq_paged_attn, OK, 1, 8, 16, 1024, None, 4, 16, 16, 4, i64, 1.0, 0, 16, 1024, None, 16, need)
+    refused(1, hq.hq_paged_attn, OK, 1, 8, 16, 1024, None, 4, 16, torch.zeros(2, 4, dtype=torch.int32).t(), 4, 16, 1.0, 0, 16,
+            1024, None, 16, need)

@@ -595,6 +595,73 @@ def test_attention_captured_with_lengths_that_change():
         check_attn(c, q, table, lens, held, 0.1, got=(out, lse))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "nvfp4"])
+def test_attention_first_call_of_a_shape_captured(dtype):
+    """The first call of a kernel may be a captured one (D = 192 with 9 heads a kv head is used nowhere else)."""
+    lens = [100, 40]
+    c, table, held = fill_cache(dtype, 1, 192, 32, lens, 95)
+    q = normal((2, 9, 192), 96, 2.0)
+    qd, ld = q.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(hq.hq_paged_attn_workspace_bytes(c.kv, 2, 9), dtype=torch.uint8, device="cuda")
+    out = torch.empty(2, 9, 192, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(2, 9, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        hq.hq_paged_attn(c.kv, 2, 9, qd, qd.stride(0), c.glob, c.pages, c.buf, table, table.shape[1], ld, 0.1, 0, out,
+                         out.stride(0), lse, ws, ws.numel())
+    for _ in range(3):
+        g.replay()
+    check_attn(c, q, table, lens, held, 0.1, got=(out, lse))
+
+
+def test_attention_two_streams_with_their_own_workspaces():
+    lens = [700, 0, 33, 1200]
+    c, table, held = fill_cache("e4m3", 2, 128, 16, lens, 97)
+    q = [normal((4, 8, 128), 98 + i, 2.0) for i in range(2)]
+    ld = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    qd, streams = [x.cuda() for x in q], [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [torch.empty(4, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    wss = [torch.zeros(hq.hq_paged_attn_workspace_bytes(c.kv, 4, 8), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    lses = [torch.empty(4, 8, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in range(2):
+            hq.hq_paged_attn(c.kv, 4, 8, qd[i], qd[i].stride(0), None, c.pages, c.buf, table, table.shape[1], ld, 0.1, 0,
+                             outs[i], outs[i].stride(0), lses[i], wss[i], wss[i].numel(), stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        check_attn(c, q[i], table, lens, held, 0.1, got=(outs[i], lses[i]))
+
+
+def test_attention_refuses_a_line_past_its_counters():
+    """2^36 tokens by page tables that name one page over and over: refused at once, and the next call is sound."""
+    c, table, held = fill_cache("e4m3", 1, 64, 4096, [50], 99, spare=0)
+    q = normal((64, 1, 64), 100, 2.0).cuda()
+    pt = torch.zeros(64, 1 << 18, dtype=torch.int32, device="cuda")
+    lens = torch.full((64,), 1 << 30, dtype=torch.int32, device="cuda")
+    lens[3] = 0
+    ws = torch.zeros(hq.hq_paged_attn_workspace_bytes(c.kv, 64, 1), dtype=torch.uint8, device="cuda")
+    out, lse = run_attn(c, q, pt, lens, 0.1, ws=ws)
+    assert hq.hq_device_error() == 2
+    assert torch.all(out[3] == 0) and torch.all(torch.isinf(lse[3]))
+    keep = [i for i in range(64) if i != 3]
+    assert torch.all(out[keep] == 7) and torch.all(lse[keep] == 7)
+    got = run_attn(c, q[:1], table, torch.tensor([50], dtype=torch.int32, device="cuda"), 0.1, ws=ws)
+    check_attn(c, q[:1].cpu(), table, [50], held, 0.1, got=got)
+
+
+def test_attention_shared_prefix_pages():
+    """Sequences may share pages (a common prompt)."""
+    c, table, held = fill_cache("nvfp4", 2, 128, 32, [64, 100], 101)
+    t = table.cpu()
+    shared = torch.stack([torch.cat([t[1, :3], t[1, 3:4]]), torch.cat([t[1, :3], t[0, :1]])]).cuda()
+    k, v = held[1]
+    other = tuple(np.concatenate([x[:96], y[:10]]) for x, y in zip(held[1], held[0]))
+    q = normal((2, 8, 128), 102, 2.0)
+    check_attn(c, q, shared, [100, 106], [(k, v), other], 0.1)
+
+
 # ---- together -------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3", "nvfp4"])
