@@ -63,8 +63,9 @@ __device__ __forceinline__ void sincos_small(float r, float &s, float &c) {
 // position (2^-53 of the frequency, 2^-64 of a turn), whose product with p
 // drops whole turns by itself; the upper 32 bits (2^-32 of a turn, 1.5e-9)
 // are brought to [-1/8, 1/8] of a turn and go through fp32 sums, an error of
-// about one fp32 step.  Bound by its stores: 131072 x 128 (67 MB) in TABLE_LONG us of
-// a floor of 10 (64-bit floating point in the loop: 21).
+// about one fp32 step.  Bound by its stores: 131072 x 128 (67 MB) in 14.9 us of
+// a floor of 10.2 (64-bit floating point in the loop: 21; one frequency a
+// thread and 4-byte stores: 18.7 with the launch).
 constexpr int TABLE_THREADS = 256;
 template <int V>
 __global__ void __launch_bounds__(TABLE_THREADS) rope_table_kernel(hq_rope_desc d, int P, float *__restrict__ table) {
@@ -269,7 +270,9 @@ inline long long rope_blocks(const RopeArgs &a) { return ((long long)a.T + a.tok
 
 // Bound by HBM: x is read and out written once, the table rows come from L2
 // (one of a token for all of its heads).  8191 tokens x 32 heads x 192 (a third rotated):
-// ROPE_PROMPT us, ROPE_RATE TB/s of the measured 6.55.
+// 35.5 us, 5.7 TB/s of the measured 6.55.  One chunk a thread and 24 warps an
+// SM beat two to four chunks (42 to 49 us), streaming loads and stores (they
+// are used once) plain ones (39.6), blocks of 128 those of 256 (37.6).
 __device__ __forceinline__ void rope_rows(const RopeArgs &a, uint32_t block) {
   const uint32_t tb = div_by(block, a.parts), part = block - tb * a.parts.d;
   const long long t0 = (long long)tb * a.tokens;
@@ -320,14 +323,6 @@ RopeArgs rope_args(int T, int H, int D, const hq_rope_desc *r, int P, const void
   const RopeSplit split = rope_split(T, per_token, threads);
   return RopeArgs{T, H, D, r->rot_dim, r->interleaved, P, (const uint16_t *)x, xt, xh, pos, table, (uint16_t *)out,
                   ot, oh, fast_div(pairs), fast_div(rest > 0 ? rest : 1), fast_div(per_token), fast_div(split.parts), split.tokens};
-}
-
-// The same rotation for blocks of another width.
-inline RopeArgs rope_resplit(RopeArgs a, int threads) {
-  const RopeSplit split = rope_split(a.T, a.per_token.d, threads);
-  a.parts = fast_div(split.parts);
-  a.tokens = split.tokens;
-  return a;
 }
 
 hq_status launch_rope(const RopeArgs &a, cudaStream_t st) {
@@ -570,11 +565,20 @@ __device__ __forceinline__ uint32_t nvfp4_octet(const float *f, uint32_t sb, flo
 // E4M3, whose scale needs a whole row.
 __host__ __device__ constexpr int kv_parts(int fmt, int D) { return fmt == A_FP8 ? 1 : D / 64; }
 
-// Bound by HBM: WRITE_NOTE
+// Two warps a group, head and part, one for keys and one for values, each with
+// a single item: what waits (slots, positions, then rows and table) is hidden
+// by the number of warps, 32 an SM at 64 registers.  With rows in registers
+// and everything unrolled, warps waited for instructions half of the time;
+// with loops over octets or heads they were too few (8191 tokens x 4 heads x
+// 256 with positions, NVFP4: 59, 28 and 30 us; this form: 21 of a floor of
+// 7).  Bound by latency and by the arithmetic of the recipe (some 200
+// instructions per octet); bf16 rows by latency alone.
 template <int FMT, int D, bool ROPE>
 __global__ void __launch_bounds__(KV_THREADS, FMT != A_FP8 ? 8 : ROPE ? 4 : 6)
     kv_write_kernel(KvArgs a, KvRows w, RopeArgs rope, unsigned kv_blocks) {
-  if (blockIdx.x >= kv_blocks) {  // these rotate the rope.H heads of q
+  // The blocks past kv_blocks rotate the rope.H heads of q (mixed in between
+  // the others, to copy beside the arithmetic, they took 12% more).
+  if (blockIdx.x >= kv_blocks) {
     rope_rows(rope, blockIdx.x - kv_blocks);
     return;
   }
@@ -847,7 +851,8 @@ __device__ __forceinline__ uint4 nvfp4_values(uint32_t w, uint32_t sb, float g) 
                     scaled_bf16x2(hmul2(e2m1x2_to_f16x2<2>(w), s), g), scaled_bf16x2(hmul2(e2m1x2_to_f16x2<3>(w), s), g));
 }
 
-// Bound by HBM: READ_NOTE
+// Bound by HBM: 32048 tokens x 8 heads x 128, E4M3: 197 MB in 34.8 us (5.7 TB/s
+// of the measured 6.55); octet by octet, with a sector for every 8 bytes: 52.
 template <int FMT, int D>
 __global__ void __launch_bounds__(KV_THREADS, 6) kv_read_kernel(KvArgs a, KvRows w) {
   constexpr int NB = D / 32, NQ = D / 64, CB = kv_code_bytes(FMT, D), SB = kv_scale_bytes(FMT, D), GS = kv_granule(FMT);
@@ -1019,16 +1024,8 @@ hq_status launch_kv_write(int fmt, int D, const KvArgs &a, const KvRows &w, cons
   return kv_dispatch(fmt, D, [&](auto F, auto DD) {
     const long long kb = kv_blocks(((long long)w.T + 15) / 16 * a.H * 2 * kv_parts(F, DD));
     if (rope.rot) {
-      // A step's q is rotated by further blocks of the launch; a prompt's by
-      // the rotation's own kernel, whose blocks are four times as many to an SM
-      // (8191 x 16 heads x 256 beside the write: FUSED us against SPLIT).
       const long long qb = rope.H ? rope_blocks(rope) : 0;
-      const bool split = qb > 148 * 4;
-      kv_write_kernel<F, DD, true><<<(unsigned)(kb + (split ? 0 : qb)), KV_THREADS, 0, st>>>(a, w, rope, (unsigned)kb);
-      if (split) {
-        const hq_status s = check_launch();
-        return s != HQ_OK ? s : launch_rope(rope_resplit(rope, ROPE_THREADS), st);
-      }
+      kv_write_kernel<F, DD, true><<<(unsigned)(kb + qb), KV_THREADS, 0, st>>>(a, w, rope, (unsigned)kb);
     } else {
       kv_write_kernel<F, DD, false><<<(unsigned)kb, KV_THREADS, 0, st>>>(a, w, rope, (unsigned)kb);
     }
