@@ -9,9 +9,9 @@
 //   * The units of all sequences and kv heads form one line, cut into equal
 //     parts for the SMs and, inside an SM, for its warps; ragged lengths
 //     therefore balance to one unit, and lengths are read on the device (a
-//     captured call serves growing sequences).  A warp streams its units
-//     through a private ring with one bulk copy each; warps meet only at the
-//     end.
+//     captured call serves growing sequences).  A warp consumes its units
+//     from a private ring that producer warps fill with one bulk copy a step;
+//     warps meet only at the end.
 //   * Tokens are the M side of m16n8k16 MMAs and the query heads the N side:
 //     S^T = K Q^T, O^T = V^T P^T.  Eight heads fill N, no row of the MMA is
 //     padding, and every cache byte is read by exactly one lane, so the cache
@@ -25,6 +25,15 @@
 //   * Parts of an item (a sequence's kv head) are joined by their log sums:
 //     warps of a CTA through shared memory, CTAs through the workspace by the
 //     last one to arrive, always in the order of the tokens.
+//
+// Measured, of the floor of one read of the attended cache at 6.55 TB/s:
+// 64 x 8192 tokens x 8 heads x 128, E4M3 (1.09 GB) 187 us under a profiler,
+// 89%; 8 x ~107000 tokens, NVFP4 (1.01 GB) 205 us, 75% (some 340 instructions
+// a unit, two thirds of the issue slots: converting codes bounds it); ragged
+// batches of 0.3 GB 47 to 67 us of floor in 62 to 82 us, 51 to 78%: some 5 us
+// to the first unit, 5 to 8 to join, and SMs that end up to 15% apart.  One
+// sequence of 4097 tokens: 14.4 us, latency (each round trip through L2 in
+// the join is 1 to 2 us).
 //
 // Arithmetic.  Scores and sums are fp32.  bf16 caches multiply in bf16 with
 // each weight split into two bf16 numbers (hi + lo, 2^-17 of the weight);
