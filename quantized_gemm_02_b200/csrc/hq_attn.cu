@@ -235,6 +235,11 @@ struct AttnSplit {
   }
 };
 
+__device__ __forceinline__ int atom_add_acq_rel(int *p, int v) {
+  int r;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(r) : "l"(p), "r"(v) : "memory");
+  return r;
+}
 __device__ __forceinline__ unsigned upto_mask(int lane) { return (2u << lane) - 1u; }
 __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {  // does not suspend the warp
   uint32_t ok;
@@ -317,8 +322,13 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
     return;
   }
   const int total = (int)sum * items;
-  const int ctas = min((total + W - 1) / W, (int)gridDim.x);  // a step per warp at least
-  if ((int)blockIdx.x >= ctas) return;
+  // A step per warp at least.  Where some warps would have two (or three, four)
+  // and others one less, all have the larger number and fewer CTAs take part:
+  // the same time for the steps, fewer records to join (1 x 4097 tokens, bf16:
+  // 13.8 us instead of 15.1).
+  const int most = max((total + W * (int)gridDim.x - 1) / (W * (int)gridDim.x), 1);
+  const int ctas = most <= 4 ? (total + most * W - 1) / (most * W) : (int)gridDim.x;
+  if (total == 0 || (int)blockIdx.x >= ctas) return;
   const int each = total / ctas;
   const AttnSplit line{each, total - each * ctas};
   const int c_begin = line.begin(blockIdx.x), c_steps = line.begin(blockIdx.x + 1) - c_begin;
@@ -926,7 +936,6 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
   // counter is that of the CTA in which the item begins.
   __syncthreads();
   if (tid == 0) {
-    int any = 0;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const AttnRun run = head->run[k ? max(runs - 1, 0) : 0];
@@ -938,16 +947,14 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
         s_from[k] = c0;
         s_from[2 + k] = n;
         s_from[4 + k] = run.first;
-        if (!any) __threadfence();
-        any = 1;
-        if (atomicAdd(&a.counters[c0], 1) == n - 1) {
+        // releases the CTA's records (ordered before by the barrier) and, for the last, acquires the others'
+        if (atom_add_acq_rel(&a.counters[c0], 1) == n - 1) {
           a.counters[c0] = 0;
           last = 1;
         }
       }
       s_last[k] = last;
     }
-    if (any) __threadfence();
   }
   __syncthreads();
   for (int k = 0; k < 2; ++k) {
