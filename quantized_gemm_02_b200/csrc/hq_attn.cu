@@ -27,9 +27,9 @@
 //     last one to arrive, always in the order of the tokens.
 //
 // Measured, of the floor of one read of the attended cache at 6.55 TB/s:
-// 64 x 8192 tokens x 8 heads x 128, E4M3 (1.09 GB) 187 us under a profiler,
-// 89%; 8 x ~107000 tokens, NVFP4 (1.01 GB) 205 us, 75% (some 340 instructions
-// a unit, two thirds of the issue slots: converting codes bounds it); ragged
+// 64 x 8192 tokens x 8 heads x 128, E4M3 (1.09 GB) 170 us under a profiler,
+// 98%; 8 x ~107000 tokens, NVFP4 (1.01 GB) 205 to 215 us, 75% (364 instructions
+// a unit, over half of the issue slots: converting codes bounds it); ragged
 // batches of 0.3 GB 47 to 67 us of floor in 62 to 82 us, 51 to 78%: some 5 us
 // to the first unit, 5 to 8 to join, and SMs that end up to 15% apart.  One
 // sequence of 4097 tokens: 14.4 us, latency (each round trip through L2 in
