@@ -347,11 +347,13 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
     int off = w_begin - head->before[lo] * items;
     for (pw.b = lo * per;; ++pw.b) {
       pw.open(a);
-      if (off < pw.nu * items) break;
+      if (off < pw.nu * items || pw.b >= a.B - 1) break;
       off -= pw.nu * items;
     }
-    pw.it = off / pw.nu;
-    pw.u = off - pw.it * pw.nu;
+    // (kept in range even if someone changes the lengths meanwhile)
+    const int nu = max(pw.nu, 1);
+    pw.it = min(off / nu, items - 1);
+    pw.u = min(off - pw.it * nu, nu - 1);
   }
 
   if (warp >= W) {

@@ -156,19 +156,21 @@ __device__ __forceinline__ void load8(const float *p, float *f) {
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
-// Work of a head: chunks of 8 pairs, then chunks of 16 unrotated channels (the
-// last may have 8 or, where pairs straddle 16-byte pieces, any number).  A
-// chunk holds both channels of its pairs, so x and out may be the same.
-inline int rope_pairs(int rot) { return (rot / 2 + 7) / 8; }
-inline int rope_rest(int D, int rot) { return (D - rot + 15) / 16; }
+// Work of a head.  rot_dim a multiple of 16: chunks of 8 pairs, then chunks of
+// 16 unrotated channels (the last may have 8).  Other widths, whose pairs
+// straddle 16-byte pieces: single pairs, then two unrotated channels at a
+// time, neighbours to neighbouring lanes.  Both channels of a pair are one
+// thread's, so x and out may be the same.
+inline bool rope_wide(int rot) { return rot % 16 == 0; }
+inline int rope_pairs(int rot) { return rope_wide(rot) ? rot / 16 : rot / 2; }
+inline int rope_rest(int D, int rot) { return rope_wide(rot) ? (D - rot + 15) / 16 : (D - rot) / 2; }
 
 // rot_dim a multiple of 16: a chunk is two 16-byte pieces (the second may be
 // missing), loaded before anything that depends on the position.
 struct RopePiece {
-  const uint16_t *x;  // the head's row, or null: no chunk
+  const uint16_t *x;  // the head's row
   uint16_t *out;
-  long long t;
-  int c, p;  // chunk, position
+  int c, p;           // chunk (or pair), position
   uint4 a, b;
 };
 __device__ __forceinline__ void rope_where(const RopePiece &r, int D, int rot, int inter, int &i0, int &i1, bool &pair) {
@@ -211,23 +213,6 @@ __device__ __forceinline__ void rope_piece(const RopePiece &r, int D, int rot, i
   __stcs(reinterpret_cast<uint4 *>(r.out + i1), pack8(b));
 }
 
-// Other widths, channel by channel.
-__device__ __noinline__ void rope_slow(int c, int D, int rot, int inter, const uint16_t *x, const float *tab, uint16_t *out) {
-  const int half = rot / 2, npair = (half + 7) / 8;
-  if (c >= npair) {
-    const int ch = rot + (c - npair) * 16;
-    for (int i = ch; i < ch + 16 && i < D; ++i) out[i] = x[i];
-    return;
-  }
-  for (int i = 8 * c; i < 8 * c + 8 && i < half; ++i) {
-    const int i0 = inter ? 2 * i : i, i1 = inter ? 2 * i + 1 : i + half;
-    float u, v;
-    rope_pair(bf16_at(x + i0), bf16_at(x + i1), tab[i], tab[half + i], u, v);
-    out[i0] = to_bf16(u);
-    out[i1] = to_bf16(v);
-  }
-}
-
 // n / d for n < 2^31 by a product: q = (umulhi(n, m) + n) >> s with
 // s = ceil(log2 d), m = floor(2^32 (2^s - d) / d) + 1.
 struct FastDiv {
@@ -254,14 +239,13 @@ struct RopeArgs {
   int tokens;                 // tokens of a block
 };
 
-// A block has up to ROPE_EACH chunks a thread: several whole tokens, or one of
-// `parts` parts of a token.
-constexpr int ROPE_EACH = 1;
+// A block has a chunk, or ROPE_NARROW single pairs, a thread: of several whole
+// tokens, or one of `parts` parts of a token.
+constexpr int ROPE_NARROW = 8;
 struct RopeSplit {
   int tokens, parts;
 };
-inline RopeSplit rope_split(int T, int per_token, int threads) {
-  const int full = ROPE_EACH * threads;
+inline RopeSplit rope_split(int T, int per_token, int full) {
   int n = full / per_token;
   if (n > T / (148 * 4)) n = T / (148 * 4);  // blocks enough for every SM come first
   return RopeSplit{n > 1 ? n : 1, (per_token + full - 1) / full};
@@ -269,48 +253,71 @@ inline RopeSplit rope_split(int T, int per_token, int threads) {
 inline long long rope_blocks(const RopeArgs &a) { return ((long long)a.T + a.tokens - 1) / a.tokens * a.parts.d; }
 
 // Bound by HBM: x is read and out written once, the table rows come from L2
-// (one of a token for all of its heads).  8191 tokens x 32 heads x 192 (a third rotated):
-// 35.5 us, 5.7 TB/s of the measured 6.55.  One chunk a thread and 24 warps an
-// SM beat two to four chunks (42 to 49 us), streaming loads and stores (they
-// are used once) plain ones (39.6), blocks of 128 those of 256 (37.6).
+// (one of a token for all of its heads).  8191 tokens x 32 heads x 192 (a third
+// rotated): 35.5 us, 5.7 TB/s of the measured 6.55.  One chunk a thread and 24
+// warps an SM beat two to four chunks (42 to 49 us), streaming loads and stores
+// (they are used once) plain ones (39.6), blocks of 128 those of 256 (37.6).
+// Single pairs (3625 x 64 x 192, 136 rotated): NARROW us of a floor of 27, bound
+// by their instructions; chunks of eight, channel by channel, took 228.
 __device__ __forceinline__ void rope_rows(const RopeArgs &a, uint32_t block) {
   const uint32_t tb = div_by(block, a.parts), part = block - tb * a.parts.d;
   const long long t0 = (long long)tb * a.tokens;
-  const uint32_t n = (uint32_t)min((long long)a.tokens, a.T - t0) * a.per_token.d;
-  const uint32_t i0 = part * ROPE_EACH * blockDim.x + threadIdx.x;
-  const bool fast = (a.rot & 15) == 0;
-  RopePiece r[ROPE_EACH];
-#pragma unroll
-  for (int u = 0; u < ROPE_EACH; ++u) {
-    const uint32_t i = i0 + u * blockDim.x;
-    r[u].x = nullptr;
-    if (i >= n) continue;
-    // a token's pairs come first, head by head, then the rest, so that warps rarely do both
-    const uint32_t tt = div_by(i, a.per_token), in = i - tt * a.per_token.d, np = a.H * a.pairs.d;
+  const uint32_t n = (uint32_t)min((long long)a.tokens, a.T - t0) * a.per_token.d, np = a.H * a.pairs.d;
+  // item i of the block: a token's pairs come first, head by head, then the
+  // rest, so that warps rarely do both
+  auto locate = [&](uint32_t i, RopePiece &r) {
+    const uint32_t tt = div_by(i, a.per_token), in = i - tt * a.per_token.d;
     const uint32_t j = in < np ? in : in - np, h = div_by(j, in < np ? a.pairs : a.rest);
-    r[u].c = in < np ? j - h * a.pairs.d : a.pairs.d + j - h * a.rest.d;
-    r[u].t = t0 + tt;
-    r[u].p = a.pos[r[u].t];
-    r[u].x = a.x + r[u].t * a.xt + h * a.xh;
-    r[u].out = a.out + r[u].t * a.ot + h * a.oh;
-    if (!fast) continue;
+    const long long t = t0 + tt;
+    r.c = in < np ? j - h * a.pairs.d : a.pairs.d + j - h * a.rest.d;
+    r.p = a.pos[t];
+    r.x = a.x + t * a.xt + h * a.xh;
+    r.out = a.out + t * a.ot + h * a.oh;
+  };
+  auto known = [&](int p) {
+    if (p >= 0 && p < a.P) return true;
+    set_device_error(HQ_ERR_DEVICE_INDEX);
+    return false;
+  };
+  if ((a.rot & 15) == 0) {
+    const uint32_t i = part * blockDim.x + threadIdx.x;
+    if (i >= n) return;
+    RopePiece r;
+    locate(i, r);
     int p0, p1;
     bool pair;
-    rope_where(r[u], a.D, a.rot, a.inter, p0, p1, pair);
-    if (!pair && r[u].x == r[u].out) continue;
-    r[u].a = __ldcs(reinterpret_cast<const uint4 *>(r[u].x + p0));
-    if (p1 >= 0) r[u].b = __ldcs(reinterpret_cast<const uint4 *>(r[u].x + p1));
+    rope_where(r, a.D, a.rot, a.inter, p0, p1, pair);
+    if (!pair && r.x == r.out) return;
+    r.a = __ldcs(reinterpret_cast<const uint4 *>(r.x + p0));
+    if (p1 >= 0) r.b = __ldcs(reinterpret_cast<const uint4 *>(r.x + p1));
+    if (known(r.p)) rope_piece(r, a.D, a.rot, a.inter, a.table + (size_t)r.p * a.rot);
+    return;
   }
-#pragma unroll
-  for (int u = 0; u < ROPE_EACH; ++u) {
-    if (!r[u].x) continue;
-    if (r[u].p < 0 || r[u].p >= a.P) {
-      set_device_error(HQ_ERR_DEVICE_INDEX);
+  const int half = a.rot / 2;
+#pragma unroll 4
+  for (int u = 0; u < ROPE_NARROW; ++u) {
+    const uint32_t i = (part * ROPE_NARROW + u) * blockDim.x + threadIdx.x;
+    if (i >= n) break;
+    RopePiece r;
+    locate(i, r);
+    if (!known(r.p)) continue;
+    if (r.c >= half) {
+      const int ch = a.rot + 2 * (r.c - half);
+      *reinterpret_cast<uint32_t *>(r.out + ch) = *reinterpret_cast<const uint32_t *>(r.x + ch);
       continue;
     }
-    const float *tab = a.table + (size_t)r[u].p * a.rot;
-    if (fast) rope_piece(r[u], a.D, a.rot, a.inter, tab);
-    else rope_slow(r[u].c, a.D, a.rot, a.inter, r[u].x, tab, r[u].out);
+    const float *tab = a.table + (size_t)r.p * a.rot;
+    const float co = tab[r.c], si = tab[half + r.c];
+    float v, w;
+    if (a.inter) {
+      const uint32_t ab = *reinterpret_cast<const uint32_t *>(r.x + 2 * r.c);
+      rope_pair(bf16_lo(ab), bf16_hi(ab), co, si, v, w);
+      *reinterpret_cast<uint32_t *>(r.out + 2 * r.c) = to_bf16x2(v, w);
+    } else {
+      rope_pair(bf16_at(r.x + r.c), bf16_at(r.x + r.c + half), co, si, v, w);
+      r.out[r.c] = to_bf16(v);
+      r.out[r.c + half] = to_bf16(w);
+    }
   }
 }
 
@@ -320,7 +327,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, 12) rope_kernel(RopeArgs a) { ro
 RopeArgs rope_args(int T, int H, int D, const hq_rope_desc *r, int P, const void *x, int64_t xt, int64_t xh,
                    const int32_t *pos, const float *table, void *out, int64_t ot, int64_t oh, int threads) {
   const int pairs = rope_pairs(r->rot_dim), rest = rope_rest(D, r->rot_dim), per_token = (pairs + rest) * (H > 0 ? H : 1);
-  const RopeSplit split = rope_split(T, per_token, threads);
+  const RopeSplit split = rope_split(T, per_token, rope_wide(r->rot_dim) ? threads : threads * ROPE_NARROW);
   return RopeArgs{T, H, D, r->rot_dim, r->interleaved, P, (const uint16_t *)x, xt, xh, pos, table, (uint16_t *)out,
                   ot, oh, fast_div(pairs), fast_div(rest > 0 ? rest : 1), fast_div(per_token), fast_div(split.parts), split.tokens};
 }
