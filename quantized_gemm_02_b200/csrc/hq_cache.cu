@@ -156,24 +156,39 @@ __device__ __forceinline__ void load8(const float *p, float *f) {
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
-// Work of a head.  rot_dim a multiple of 16: chunks of 8 pairs, then chunks of
-// 16 unrotated channels (the last may have 8).  Other widths, whose pairs
-// straddle 16-byte pieces: single pairs, then two unrotated channels at a
-// time, neighbours to neighbouring lanes.  Both channels of a pair are one
-// thread's, so x and out may be the same.
-inline bool rope_wide(int rot) { return rot % 16 == 0; }
-inline int rope_pairs(int rot) { return rope_wide(rot) ? rot / 16 : rot / 2; }
-inline int rope_rest(int D, int rot) { return rope_wide(rot) ? (D - rot + 15) / 16 : (D - rot) / 2; }
+// Work of a head.  Interleaved pairs, and halves of a multiple of 8: chunks of
+// 8 pairs, then chunks of 16 unrotated channels (the last may have 8; the last
+// of interleaved pairs may end with unrotated channels).  Halves of another
+// width, whose pairs straddle 16-byte pieces: single pairs, then two unrotated
+// channels at a time, neighbours to neighbouring lanes.  Both channels of a
+// pair are one thread's, so x and out may be the same.
+enum RopeWidth { ROPE_EVEN, ROPE_RAGGED, ROPE_SINGLE };
+__host__ __device__ inline RopeWidth rope_width(int rot, int inter) {
+  return rot % 16 == 0 ? ROPE_EVEN : inter ? ROPE_RAGGED : ROPE_SINGLE;
+}
+inline int rope_pairs(int rot, int inter) { return rope_width(rot, inter) == ROPE_SINGLE ? rot / 2 : (rot + 15) / 16; }
+inline int rope_rest(int D, int rot, int inter) {
+  if (rope_width(rot, inter) == ROPE_SINGLE) return (D - rot) / 2;
+  const int left = D - 16 * rope_pairs(rot, inter);
+  return left > 0 ? (left + 15) / 16 : 0;
+}
 
-// rot_dim a multiple of 16: a chunk is two 16-byte pieces (the second may be
-// missing), loaded before anything that depends on the position.
+// A chunk is two 16-byte pieces (the second may be missing), loaded before
+// anything that depends on the position.
 struct RopePiece {
   const uint16_t *x;  // the head's row
   uint16_t *out;
   int c, p;           // chunk (or pair), position
   uint4 a, b;
 };
+template <RopeWidth W>
 __device__ __forceinline__ void rope_where(const RopePiece &r, int D, int rot, int inter, int &i0, int &i1, bool &pair) {
+  if constexpr (W == ROPE_RAGGED) {
+    pair = r.c < (rot + 15) / 16;
+    i0 = 16 * r.c;
+    i1 = i0 + 8 < D ? i0 + 8 : -1;
+    return;
+  }
   const int half = rot / 2, npair = half / 8;
   pair = r.c < npair;
   if (pair) {
@@ -184,10 +199,11 @@ __device__ __forceinline__ void rope_where(const RopePiece &r, int D, int rot, i
     i1 = i0 + 8 < D ? i0 + 8 : -1;
   }
 }
+template <RopeWidth W>
 __device__ __forceinline__ void rope_piece(const RopePiece &r, int D, int rot, int inter, const float *tab) {
   int i0, i1;
   bool pair;
-  rope_where(r, D, rot, inter, i0, i1, pair);
+  rope_where<W>(r, D, rot, inter, i0, i1, pair);
   if (!pair) {
     if (r.x == r.out) return;
     __stcs(reinterpret_cast<uint4 *>(r.out + i0), r.a);
@@ -197,20 +213,35 @@ __device__ __forceinline__ void rope_piece(const RopePiece &r, int D, int rot, i
   float a[8], b[8], co[8], si[8];
   unpack8(r.a, a);
   unpack8(r.b, b);
-  load8(tab + 8 * r.c, co);
-  load8(tab + rot / 2 + 8 * r.c, si);
-  if (inter) {
+  const int half = rot / 2;
+  if constexpr (W == ROPE_RAGGED) {  // rows of the table are not 16-byte aligned
+    const int n = half - 8 * r.c;    // pairs that are rotated
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      co[j] = j < n ? tab[8 * r.c + j] : 0.f;
+      si[j] = j < n ? tab[half + 8 * r.c + j] : 0.f;
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      rope_pair(a[2 * j], a[2 * j + 1], co[j], si[j], a[2 * j], a[2 * j + 1]);
-      rope_pair(b[2 * j], b[2 * j + 1], co[4 + j], si[4 + j], b[2 * j], b[2 * j + 1]);
+      if (j < n) rope_pair(a[2 * j], a[2 * j + 1], co[j], si[j], a[2 * j], a[2 * j + 1]);
+      if (4 + j < n) rope_pair(b[2 * j], b[2 * j + 1], co[4 + j], si[4 + j], b[2 * j], b[2 * j + 1]);
     }
   } else {
+    load8(tab + 8 * r.c, co);
+    load8(tab + half + 8 * r.c, si);
+    if (inter) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) rope_pair(a[j], b[j], co[j], si[j], a[j], b[j]);
+      for (int j = 0; j < 4; ++j) {
+        rope_pair(a[2 * j], a[2 * j + 1], co[j], si[j], a[2 * j], a[2 * j + 1]);
+        rope_pair(b[2 * j], b[2 * j + 1], co[4 + j], si[4 + j], b[2 * j], b[2 * j + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) rope_pair(a[j], b[j], co[j], si[j], a[j], b[j]);
+    }
   }
   __stcs(reinterpret_cast<uint4 *>(r.out + i0), pack8(a));
-  __stcs(reinterpret_cast<uint4 *>(r.out + i1), pack8(b));
+  if (W == ROPE_EVEN || i1 >= 0) __stcs(reinterpret_cast<uint4 *>(r.out + i1), pack8(b));
 }
 
 // n / d for n < 2^31 by a product: q = (umulhi(n, m) + n) >> s with
@@ -254,11 +285,14 @@ inline long long rope_blocks(const RopeArgs &a) { return ((long long)a.T + a.tok
 
 // Bound by HBM: x is read and out written once, the table rows come from L2
 // (one of a token for all of its heads).  8191 tokens x 32 heads x 192 (a third
-// rotated): 35.5 us, 5.7 TB/s of the measured 6.55.  One chunk a thread and 24
+// rotated): 37.0 us, 5.5 TB/s of the measured 6.55.  One chunk a thread and 24
 // warps an SM beat two to four chunks (42 to 49 us), streaming loads and stores
 // (they are used once) plain ones (39.6), blocks of 128 those of 256 (37.6).
-// Single pairs (3625 x 64 x 192, 136 rotated): NARROW us of a floor of 27, bound
-// by their instructions; chunks of eight, channel by channel, took 228.
+// Of 136 rotated (3625 x 64 x 192, a floor of 27 us) interleaved pairs take 36,
+// in single pairs 89; halves take 75, in single pairs bound by their
+// instructions, and in chunks of eight read channel by channel 228.  A kernel
+// for each width: sharing one, the ragged code cost the even widths 6%.
+template <RopeWidth W>
 __device__ __forceinline__ void rope_rows(const RopeArgs &a, uint32_t block) {
   const uint32_t tb = div_by(block, a.parts), part = block - tb * a.parts.d;
   const long long t0 = (long long)tb * a.tokens;
@@ -279,18 +313,18 @@ __device__ __forceinline__ void rope_rows(const RopeArgs &a, uint32_t block) {
     set_device_error(HQ_ERR_DEVICE_INDEX);
     return false;
   };
-  if ((a.rot & 15) == 0) {
+  if constexpr (W != ROPE_SINGLE) {
     const uint32_t i = part * blockDim.x + threadIdx.x;
     if (i >= n) return;
     RopePiece r;
     locate(i, r);
     int p0, p1;
     bool pair;
-    rope_where(r, a.D, a.rot, a.inter, p0, p1, pair);
+    rope_where<W>(r, a.D, a.rot, a.inter, p0, p1, pair);
     if (!pair && r.x == r.out) return;
     r.a = __ldcs(reinterpret_cast<const uint4 *>(r.x + p0));
     if (p1 >= 0) r.b = __ldcs(reinterpret_cast<const uint4 *>(r.x + p1));
-    if (known(r.p)) rope_piece(r, a.D, a.rot, a.inter, a.table + (size_t)r.p * a.rot);
+    if (known(r.p)) rope_piece<W>(r, a.D, a.rot, a.inter, a.table + (size_t)r.p * a.rot);
     return;
   }
   const int half = a.rot / 2;
@@ -309,31 +343,31 @@ __device__ __forceinline__ void rope_rows(const RopeArgs &a, uint32_t block) {
     const float *tab = a.table + (size_t)r.p * a.rot;
     const float co = tab[r.c], si = tab[half + r.c];
     float v, w;
-    if (a.inter) {
-      const uint32_t ab = *reinterpret_cast<const uint32_t *>(r.x + 2 * r.c);
-      rope_pair(bf16_lo(ab), bf16_hi(ab), co, si, v, w);
-      *reinterpret_cast<uint32_t *>(r.out + 2 * r.c) = to_bf16x2(v, w);
-    } else {
-      rope_pair(bf16_at(r.x + r.c), bf16_at(r.x + r.c + half), co, si, v, w);
-      r.out[r.c] = to_bf16(v);
-      r.out[r.c + half] = to_bf16(w);
-    }
+    rope_pair(bf16_at(r.x + r.c), bf16_at(r.x + r.c + half), co, si, v, w);
+    r.out[r.c] = to_bf16(v);
+    r.out[r.c + half] = to_bf16(w);
   }
 }
 
 constexpr int ROPE_THREADS = 128;
-__global__ void __launch_bounds__(ROPE_THREADS, 12) rope_kernel(RopeArgs a) { rope_rows(a, blockIdx.x); }
+template <RopeWidth W>
+__global__ void __launch_bounds__(ROPE_THREADS, W == ROPE_EVEN ? 12 : W == ROPE_RAGGED ? 10 : 8) rope_kernel(RopeArgs a) {
+  rope_rows<W>(a, blockIdx.x);
+}
 
 RopeArgs rope_args(int T, int H, int D, const hq_rope_desc *r, int P, const void *x, int64_t xt, int64_t xh,
                    const int32_t *pos, const float *table, void *out, int64_t ot, int64_t oh, int threads) {
-  const int pairs = rope_pairs(r->rot_dim), rest = rope_rest(D, r->rot_dim), per_token = (pairs + rest) * (H > 0 ? H : 1);
-  const RopeSplit split = rope_split(T, per_token, rope_wide(r->rot_dim) ? threads : threads * ROPE_NARROW);
+  const int pairs = rope_pairs(r->rot_dim, r->interleaved), rest = rope_rest(D, r->rot_dim, r->interleaved);
+  const int per_token = (pairs + rest) * (H > 0 ? H : 1);
+  const RopeSplit split = rope_split(T, per_token, rope_width(r->rot_dim, r->interleaved) == ROPE_SINGLE ? threads * ROPE_NARROW : threads);
   return RopeArgs{T, H, D, r->rot_dim, r->interleaved, P, (const uint16_t *)x, xt, xh, pos, table, (uint16_t *)out,
                   ot, oh, fast_div(pairs), fast_div(rest > 0 ? rest : 1), fast_div(per_token), fast_div(split.parts), split.tokens};
 }
 
 hq_status launch_rope(const RopeArgs &a, cudaStream_t st) {
-  rope_kernel<<<(unsigned)rope_blocks(a), ROPE_THREADS, 0, st>>>(a);
+  const RopeWidth w = rope_width(a.rot, a.inter);
+  auto *const kernel = w == ROPE_EVEN ? rope_kernel<ROPE_EVEN> : w == ROPE_RAGGED ? rope_kernel<ROPE_RAGGED> : rope_kernel<ROPE_SINGLE>;
+  kernel<<<(unsigned)rope_blocks(a), ROPE_THREADS, 0, st>>>(a);
   return check_launch();
 }
 
@@ -586,7 +620,10 @@ __global__ void __launch_bounds__(KV_THREADS, FMT != A_FP8 ? 8 : ROPE ? 4 : 6)
   // The blocks past kv_blocks rotate the rope.H heads of q (mixed in between
   // the others, to copy beside the arithmetic, they took 12% more).
   if (blockIdx.x >= kv_blocks) {
-    rope_rows(rope, blockIdx.x - kv_blocks);
+    const RopeWidth w = rope_width(rope.rot, rope.inter);
+    if (w == ROPE_EVEN) rope_rows<ROPE_EVEN>(rope, blockIdx.x - kv_blocks);
+    else if (w == ROPE_RAGGED) rope_rows<ROPE_RAGGED>(rope, blockIdx.x - kv_blocks);
+    else rope_rows<ROPE_SINGLE>(rope, blockIdx.x - kv_blocks);
     return;
   }
   constexpr int NB = D / 32, NQ = D / 64, CB = kv_code_bytes(FMT, D), SB = kv_scale_bytes(FMT, D), GS = kv_granule(FMT);

@@ -132,7 +132,8 @@ def tab64(f, P):
 @pytest.mark.parametrize("inter", [0, 1])
 @pytest.mark.parametrize("T,H,D,rot,gap", [
     (1, 1, 64, 64, 0), (3, 5, 128, 128, 64), (7, 2, 192, 64, 8), (5, 3, 256, 48, 0), (33, 1, 128, 10, 0), (4, 2, 8, 2, 0),
-    (6, 2, 40, 36, 16), (300, 9, 96, 96, 32),
+    (6, 2, 40, 36, 16), (300, 9, 96, 96, 32), (5, 3, 24, 16, 0), (5, 3, 24, 18, 8), (9, 4, 256, 250, 0), (700, 2, 64, 34, 0),
+    (40, 5, 192, 130, 8),
 ])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_rope(inter, T, H, D, rot, gap, in_place):
