@@ -362,8 +362,8 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
     uint32_t parity = 1;
     const int upp = a.kv.page_units;
     const int32_t *pages = a.page_table;
-    // The pages of the step's units.  Entries before the window or past the
-    // length are not used; the second unit may be on the next page.
+    // The pages of the step's units.  Entries before the window are not used,
+    // those past the length not read; the second unit may be on the next page.
     auto fetch = [&](bool turned) {
       if (turned) {
         pages = a.page_table + (size_t)pw.b * a.max_pages;
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
         }
       }
       const int at = (pw.u0 + pw.u) * TOK;
-      pg[0] = STEP == 1 || at + 16 > pw.first ? pages[pidx] : -1;
+      pg[0] = pages[pidx];  // (also where the window begins in the second unit: later steps are on this page)
       if constexpr (STEP == 2) pg[1] = at + 16 >= pw.len ? -1 : psub + 1 < upp ? pages[pidx] : pages[pidx + 1];
     };
     if (to_issue > 0) fetch(true);

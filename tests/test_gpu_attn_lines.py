@@ -1,0 +1,152 @@
+"""Attention over the paged cache where a warp walks many steps, against 64-bit computations on the device.
+
+The units of all sequences and kv heads form one line that is cut over some 450 to 2100 warps; the cases here are
+longer than that, so that warps go from page to page, from item to item and around their rings."""
+import math
+
+import pytest
+import torch
+
+import quantized_gemm_02_b200 as hq
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": hq.HQ_BF16, "e4m3": hq.HQ_E4M3, "nvfp4": hq.HQ_NVFP4}
+GLOB = (6.0 / 2688.0, 5.0 / 2688.0)
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def normal(shape, seed, scale=1.0):
+    return (torch.randn(shape, generator=gen(seed), device="cuda") * scale).to(torch.bfloat16)
+
+
+def held64(x, dtype, g):
+    """What a cache holds of bf16 x [.., D], in 64 bits; the recipes' steps are fp32 divisions by tensors."""
+    if dtype == "bf16":
+        return x.double()
+    x, c = x.float(), lambda v: torch.tensor(v, device="cuda")  # noqa: E731
+    if dtype == "e4m3":
+        s = x.abs().amax(-1, keepdim=True) / c(448.0)
+        s = torch.where(s == 0, torch.ones_like(s), s)
+        return (x / s).clamp(-448, 448).to(torch.float8_e4m3fn).double() * s.double()
+    b = x.unflatten(-1, (-1, 16))
+    sb = (b.abs().amax(-1, keepdim=True) / c(6.0) / c(g)).clamp(max=448).to(torch.float8_e4m3fn).float()
+    d = sb * c(g)
+    y = torch.where(d == 0, torch.zeros_like(b), b / d)
+    a = y.abs()
+    step = torch.where(a < 2, 0.5, torch.where(a < 4, 1.0, 2.0))
+    e = torch.copysign((torch.round(a / step) * step).clamp(max=6), y)
+    return (e.double() * sb.double() * c(g).double()).flatten(-2)
+
+
+class Paged:
+    """A cache whose sequences b hold tokens [first[b], lens[b]) on pages in random order; what else is in the pages
+    is NaN codes, and the table's entries of pages that are not held are out of range."""
+
+    def __init__(self, dtype, H, D, page, lens, first, seed, make=None):
+        self.dtype, self.H, self.D, self.page, self.lens, self.first = dtype, H, D, page, lens, first
+        spans = [(f // page, -(-n // page)) if n > f else (0, 0) for f, n in zip(first, lens)]
+        used = sum(e - s for s, e in spans)
+        self.pages = used + 1
+        self.kv = hq.KVDesc(dtype=DT[dtype], heads=H, head_dim=D, page_size=page)
+        self.buf = torch.full((self.pages * hq.hq_kv_page_bytes(self.kv),), 0xFF, dtype=torch.uint8, device="cuda")
+        self.glob = torch.tensor(GLOB, device="cuda") if dtype == "nvfp4" else None
+        perm = torch.randperm(self.pages, generator=torch.Generator().manual_seed(seed)).to(torch.int32)
+        table = torch.empty(len(lens), max(max(e for _, e in spans), 1), dtype=torch.int32)
+        table[:, ::2], table[:, 1::2] = -1, 1 << 30
+        at, seqs, toks = 0, [], []
+        for b, (s, e) in enumerate(spans):
+            table[b, s:e] = perm[at:at + e - s]
+            at += e - s
+            toks.append(torch.arange(first[b], max(lens[b], first[b])))
+            seqs.append(torch.full_like(toks[-1], b))
+        seqs, toks = torch.cat(seqs), torch.cat(toks)
+        slots = (table[seqs, toks // page].long() * page + toks % page).cuda()
+        n = slots.numel()
+        self.k, self.v = make(seqs.cuda(), toks.cuda()) if make else (normal((n, H, D), seed + 1), normal((n, H, D), seed + 2))
+        hq.hq_kv_write(self.kv, n, self.k, H * D, self.v, H * D, slots, self.glob, self.pages, self.buf)
+        self.table, self.ld = table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+        self.ends = [0]
+        for f, m in zip(first, lens):
+            self.ends.append(self.ends[-1] + max(m - f, 0))
+
+    def call(self, q, scale, window=0, ws=None):
+        B, Hq, D = q.shape
+        need = hq.hq_paged_attn_workspace_bytes(self.kv, B, Hq)
+        ws = torch.zeros(need, dtype=torch.uint8, device="cuda") if ws is None else ws
+        out = torch.full((B, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((B, Hq), 7.0, device="cuda")
+        hq.hq_paged_attn(self.kv, B, Hq, q, q.stride(0), self.glob, self.pages, self.buf, self.table, self.table.shape[1],
+                         self.ld, scale, window, out, out.stride(0), lse, ws, ws.numel())
+        return out, lse
+
+    def check(self, q, scale, window=0):
+        """Calls twice (the results are the same bit for bit) and compares with the formula."""
+        ws = torch.zeros(hq.hq_paged_attn_workspace_bytes(self.kv, q.shape[0], q.shape[1]), dtype=torch.uint8, device="cuda")
+        out, lse = self.call(q, scale, window, ws)
+        again = self.call(q, scale, window, ws)
+        assert hq.hq_device_error() == 0
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+        G = q.shape[1] // self.H
+        worst = []
+        for b, n in enumerate(self.lens):
+            first = max(n - window, 0) if window else 0
+            assert n == 0 or first >= self.first[b]
+            if n == 0:
+                assert torch.all(out[b] == 0) and torch.all(lse[b] == -math.inf)
+                continue
+            rows = slice(self.ends[b] + first - self.first[b], self.ends[b + 1])
+            k, v = held64(self.k[rows], self.dtype, GLOB[0]), held64(self.v[rows], self.dtype, GLOB[1])
+            for h in range(self.H):
+                worst.append(self._compare(q[b, h * G:(h + 1) * G].double(), k[:, h], v[:, h], scale,
+                                           out[b, h * G:(h + 1) * G].double(), lse[b, h * G:(h + 1) * G].double()))
+        w = torch.stack(worst).amax(0).tolist()
+        assert w[0] <= 1 and w[1] <= 1, w
+
+    def _compare(self, q, k, v, scale, out, lse):
+        """Errors of out and lse, each as a share of its bound."""
+        x = scale * (q @ k.T)
+        wl = torch.logsumexp(x, -1)
+        p = torch.exp(x - wl[:, None])
+        want, mag = p @ v, p @ v.abs()
+        # A score: at most 32 fp32 accumulations, each off by up to 2^-23 of sum |q k| (a tensor core may truncate), and a
+        # handful of fp32 products and sums: 2^-18 of the largest sum |q k|.
+        dx = 2.0**-18 * abs(scale) * (q.abs() @ k.abs().T).amax(-1)
+        # Output: that much of each weight, twice (numerator and denominator); 2^-11 for weights in fp16 and as much for
+        # exp and the sums; its own rounding to bf16, 2^-8.  fp16 weights end at a spacing of 2^-24 where the largest one
+        # (E4M3: times its token's scale) is at least 2^10: 2^-35 of that from every token.
+        small = torch.zeros_like(wl)
+        if self.dtype != "bf16":
+            top = v.abs().max() if self.dtype == "nvfp4" else (p * v.abs().amax(-1)).amax(-1)
+            small = k.shape[0] * 2.0**-35 * top * torch.ones_like(wl)
+        tol = 2.0**-8 * want.abs() + (2.0**-10 + 2 * dx[:, None]) * mag + small[:, None] + 1e-37
+        ltol = 2.0**-20 * (1 + wl.abs()) + dx
+        return torch.stack([((out - want).abs() / tol).max(), ((lse - wl).abs() / ltol).max()]).nan_to_num(nan=math.inf)
+
+
+FORMS = [("nvfp4", 64), ("nvfp4", 128), ("nvfp4", 192), ("nvfp4", 256), ("e4m3", 64), ("e4m3", 128), ("bf16", 64)]
+
+
+@pytest.mark.parametrize("dtype,D", FORMS)
+@pytest.mark.parametrize("page", [16, 48, 64, 80, 128, 512])
+def test_window_that_begins_anywhere(dtype, D, page):
+    """256 sequences whose windows begin at every offset in a step; pages before a window are gone."""
+    window = 1000
+    lens = [window + b + 64 * (b % 5) for b in range(250)] + [1, 999, 0, 17, 1000, 0]
+    first = [max(0, n - window) for n in lens]
+    c = Paged(dtype, 8, D, page, lens, first, 1)
+    c.check(normal((len(lens), 32, D), 5, 1.0), 1.0 / math.sqrt(D), window)
+
+
+@pytest.mark.parametrize("window", [1, 15, 31, 33, 128, 3001])
+@pytest.mark.parametrize("dtype,D,G", [("nvfp4", 128, 12), ("e4m3", 64, 3), ("bf16", 128, 4)])
+def test_windows_of_other_lengths(dtype, D, G, window):
+    """Short windows have many items a warp, a long one several steps of an item; lengths of every residue."""
+    B = 600 if window < 1000 else 80
+    lens = [1 + (b * 37) % 4500 for b in range(B)]
+    first = [max(0, n - window) for n in lens]
+    c = Paged(dtype, 2, D, 64, lens, first, 11)
+    c.check(normal((B, 2 * G, D), 12, 1.0), 1.0 / math.sqrt(D), window)
