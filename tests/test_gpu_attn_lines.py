@@ -150,3 +150,76 @@ def test_windows_of_other_lengths(dtype, D, G, window):
     first = [max(0, n - window) for n in lens]
     c = Paged(dtype, 2, D, 64, lens, first, 11)
     c.check(normal((B, 2 * G, D), 12, 1.0), 1.0 / math.sqrt(D), window)
+
+
+# What the cases below reach (a step is 16 or 32 tokens of a kv head; there are 3 to 14 warps a CTA):
+#   ragged       several steps a warp, items that a warp begins, ends or holds whole, two records of a warp, items over
+#                several CTAs, one to four equal steps a warp and more, pages that end inside a step
+#   many         whole items by the dozen in a warp, shares of two and more sequences in the scan, empty ones among them
+#   one_item     every warp goes around its ring (at least STAGES + 2 steps), one item over all CTAs
+#   growing      the references move in nearly every step
+
+SHAPES = [(dtype, D, G) for dtype in DT for D in (64, 128, 192, 256) for G in (5, 12)]
+
+
+@pytest.mark.parametrize("dtype,D,G", SHAPES)
+@pytest.mark.parametrize("page", [16, 48, 128])
+def test_ragged_lines(dtype, D, G, page):
+    lens = [4001, 0, 1, 15, 16, 17, 31, 32, 33, 700, 3333, 2048] + [97 * i + 40 for i in range(24)]
+    c = Paged(dtype, 8, D, page, lens, [0] * len(lens), 21)
+    c.check(normal((len(lens), 8 * G, D), 22, 1.0), 1.0 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("dtype,D,G", [("bf16", 256, 4), ("e4m3", 128, 8), ("nvfp4", 128, 8), ("e4m3", 192, 16), ("nvfp4", 64, 16)])
+@pytest.mark.parametrize("n", [1999, 4500, 9001, 17000, 26000, 34567, 52000])
+def test_steps_a_warp(dtype, D, G, n):
+    """The same number of steps in every warp, up to four, and more beyond: one long sequence beside a short one."""
+    c = Paged(dtype, 8, D, 64, [7, n], [0, 0], 31)
+    c.check(normal((2, 8 * G, D), 32, 1.0), 1.0 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("dtype,D,G", [("bf16", 128, 8), ("e4m3", 64, 2), ("nvfp4", 128, 16), ("e4m3", 256, 9), ("nvfp4", 256, 1)])
+@pytest.mark.parametrize("B", [513, 1000])
+def test_many_items(dtype, D, G, B):
+    lens = [(b * 53) % 171 for b in range(B)]
+    c = Paged(dtype, 4, D, 32, lens, [0] * B, 41)
+    c.check(normal((B, 4 * G, D), 42, 1.0), 1.0 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("dtype,D,G", SHAPES)
+def test_one_item_over_the_whole_machine(dtype, D, G):
+    """Head i sees little but the units whose number is i modulo 16, and a value is not 0 in the channel of
+    (number / 16) modulo D alone: a unit that is left out, taken twice or exchanged is a large part of a result."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n = sms * 14 * 14 * (32 if dtype == "nvfp4" or (dtype, D) == ("e4m3", 64) else 16) + 21
+
+    def make(seqs, toks):
+        u = toks // 16
+        k = normal((n, 1, D), 51, 0.01)
+        k[torch.arange(n, device="cuda"), 0, u % 16] = 4.0
+        v = torch.zeros(n, 1, D, dtype=torch.bfloat16, device="cuda")
+        v[torch.arange(n, device="cuda"), 0, u // 16 % D] = 1.0 + normal((n,), 52).abs()
+        return k, v
+
+    c = Paged(dtype, 1, D, 256, [n], [0], 50, make)
+    q = normal((1, G, D), 53, 0.01)
+    q[0, torch.arange(G), torch.arange(G)] = 3.0
+    c.check(q, 1.0)
+
+
+@pytest.mark.parametrize("dtype,D,G", [("bf16", 64, 8), ("bf16", 256, 16), ("e4m3", 128, 8), ("e4m3", 64, 16), ("nvfp4", 128, 8),
+                                       ("nvfp4", 192, 16)])
+def test_scores_that_grow(dtype, D, G):
+    """Scores that rise by some hundreds along each sequence, and for half of the heads fall."""
+    lens = [3001, 20000, 1, 513, 9999]
+    total = sum(lens)
+
+    def make(seqs, toks):
+        k, v = normal((total, 4, D), 61), normal((total, 4, D), 62)
+        k[:, :, 0] = (5.0 * toks / torch.tensor(lens, device="cuda")[seqs]).to(torch.bfloat16)[:, None]
+        return k, v
+
+    c = Paged(dtype, 4, D, 64, lens, [0] * len(lens), 60, make)
+    q = normal((len(lens), 4 * G, D), 63, 1.0)
+    q[:, ::2, 0], q[:, 1::2, 0] = 600.0, -600.0
+    c.check(q, 0.125)
