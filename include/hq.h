@@ -480,12 +480,14 @@ typedef struct {
   double base;         /* > 1                                                                  */
   double factor;       /* > 0 (LINEAR, TURNS, INDEX)                                           */
   double low, high;    /* turns, 0 < low < high (TURNS, INDEX)                                 */
-  double amplitude;    /* multiplies cosine and sine; 0 = 1                                    */
+  double amplitude;    /* multiplies cosine and sine; 0 = 1; below 1e30                        */
 } hq_rope_desc;
 
 /* table fp32 [P, rot_dim]: row p holds amplitude * cos(p f'_i) for
- * i < rot_dim / 2, then amplitude * sin(p f'_i); angles in 64 bits, reduced
- * before they are rounded.  Built once; P >= 0. */
+ * i < rot_dim / 2, then amplitude * sin(p f'_i).  Angles are fractions of a
+ * turn in 64 bits: an entry is off by at most 5 * 2^-24 of itself, and by what
+ * 2^-64 of a turn and 2^-51 of the frequency make of its angle over p
+ * positions.  Built once; P >= 0. */
 HQ_API hq_status hq_rope_table(const hq_rope_desc *rope, int P, float *table, hq_stream_t stream);
 
 /* Rotates x [T, H, D] into out [T, H, D]: with c, s from row positions[t]

@@ -736,7 +736,8 @@ static hq_status check_pages(const hq_kv_desc *kv, int num_pages, const void *pa
 
 hq_status hq_rope_table(const hq_rope_desc *rope, int P, float *table, hq_stream_t stream) {
   if (!rope || !valid_rope(rope, 1024) || P < 0) return HQ_ERR_INVALID_ARG;
-  if (!(rope->base > 1.0) || !(rope->base < 1e30) || !(rope->amplitude >= 0.0)) return HQ_ERR_INVALID_ARG;
+  if (!(rope->base > 1.0) || !(rope->base < 1e30) || !(rope->amplitude >= 0.0) || !(rope->amplitude < 1e30))
+    return HQ_ERR_INVALID_ARG;
   if (rope->scaling < HQ_ROPE_PLAIN || rope->scaling > HQ_ROPE_INDEX) return HQ_ERR_UNSUPPORTED;
   if (rope->scaling != HQ_ROPE_PLAIN && !(rope->factor > 0.0)) return HQ_ERR_INVALID_ARG;
   if (rope->scaling >= HQ_ROPE_TURNS && (!(rope->low > 0.0) || !(rope->high > rope->low) || rope->context < 1))

@@ -49,29 +49,47 @@ __device__ __forceinline__ double rope_freq(const hq_rope_desc &d, int i) {
   return f;
 }
 
-// Sine and cosine of |r| <= pi / 4 by their Taylor sums, to r^9 and r^10: what
-// is left out is under 2e-9, a thirtieth of an fp32 step.
-__device__ __forceinline__ void sincos_small(float r, float &s, float &c) {
+// amplitude * (cosine, sine) of a 64-bit fraction of a turn, within an fp32
+// step of the value.  Whole quarters come off (Q); what is left, in units of
+// 2^-32 of a turn, is t + d: t a multiple of 32 that fp32 holds, d the rest with
+// 27 bits behind the point, so that small angles keep their bits.  r is the
+// rounded t in radians and e what r lacks of the angle.  The polynomials are
+// minimax fits for |r| <= pi / 4 (a linear program over 4001 points), off by
+// 5.5e-9 of the sine and 6e-10, a tenth of a step; sine and cosine go on as r + u
+// and 1 + w, and the product with the amplitude (amp + amp_rest) is rounded
+// where the large part comes in.
+__device__ __forceinline__ void turn_cos_sin(unsigned long long turn, float amp, float amp_rest, float &co, float &si) {
+  const uint32_t hi = (uint32_t)(turn >> 32), lo = (uint32_t)turn, Q = (hi + (1u << 29)) & 0xC0000000u;
+  const uint32_t h = hi - Q + 16u;
+  const float t = (float)(int)(h & ~31u), d = (float)(int)(((h << 27) | (lo >> 5)) ^ 0x80000000u);
+  constexpr float C = 6.283185307179586f / 4294967296.f;  // radians a unit, and what it lacks
+  constexpr float C_REST = (float)(6.283185307179586 / 4294967296.0 - (double)C);
+  const float r = t * C, e = fmaf(d, C / 134217728.f, fmaf(t, C_REST, fmaf(t, C, -r)));
   const float z = r * r;
-  s = fmaf(fmaf(fmaf(fmaf(z, 1.f / 362880.f, -1.f / 5040.f), z, 1.f / 120.f), z, -1.f / 6.f), z * r, r);
-  c = fmaf(fmaf(fmaf(fmaf(fmaf(z, -1.f / 3628800.f, 1.f / 40320.f), z, -1.f / 720.f), z, 1.f / 24.f), z, -0.5f), z, 1.f);
+  const float p = fmaf(fmaf(z, -1.9517266e-4f, 8.332178e-3f), z, -1.6666655e-1f);                 // (sin r - r) / r^3
+  const float q = fmaf(fmaf(fmaf(z, 2.4438406e-5f, -1.3887368e-3f), z, 4.1666646e-2f), z, -0.5f);  // (cos r - 1) / r^2
+  const float u = fmaf(p * z, r, e), w = fmaf(q, z, -e * r);
+  const float s = fmaf(amp, r, fmaf(amp, u, amp_rest * r)), c = amp + fmaf(amp, w, amp_rest);
+  const bool odd = Q & 0x40000000u;
+  si = __uint_as_float(__float_as_uint(odd ? c : s) ^ (Q & 0x80000000u));
+  co = __uint_as_float(__float_as_uint(odd ? s : c) ^ ((Q + 0x40000000u) & 0x80000000u));
 }
 
 // table[p] = amplitude * (cos(p f_0) .. cos(p f_{R/2-1}), sin(p f_0) ..).  The
 // angle of a far position does not fit fp32 (position 131072 leaves 2^-7 of a
 // radian there).  It is counted in turns, as a 64-bit binary fraction per
 // position (2^-53 of the frequency, 2^-64 of a turn), whose product with p
-// drops whole turns by itself; the upper 32 bits (2^-32 of a turn, 1.5e-9)
-// are brought to [-1/8, 1/8] of a turn and go through fp32 sums, an error of
-// about one fp32 step.  Bound by its stores: 131072 x 128 (67 MB) in 14.9 us of
-// a floor of 10.2 (64-bit floating point in the loop: 21; one frequency a
-// thread and 4-byte stores: 18.7 with the launch).
-constexpr int TABLE_THREADS = 256;
+// drops whole turns by itself.  131072 x 128 (67 MB) takes 14.6 us of a floor of
+// 10.2: 3 until the blocks have their frequencies (64-bit powers), then some 45
+// instructions an angle beside the stores (64-bit floating point in the loop:
+// 21).  The powers take 64 registers, so four blocks an SM are resident; a
+// grid of twice that computes the frequencies a second time behind them: 16.5.
+constexpr int TABLE_THREADS = 256, TABLE_BLOCKS = 4;  // of an SM
 template <int V>
-__global__ void __launch_bounds__(TABLE_THREADS) rope_table_kernel(hq_rope_desc d, int P, float *__restrict__ table) {
+__global__ void __launch_bounds__(TABLE_THREADS, TABLE_BLOCKS) rope_table_kernel(hq_rope_desc d, int P, float *__restrict__ table) {
   __shared__ unsigned long long per[512];  // turns per position, times 2^64
   const int half = d.rot_dim / 2;
-  const float amp = (float)d.amplitude;
+  const float amp = (float)d.amplitude, amp_rest = (float)(d.amplitude - (double)amp);
   for (int i = threadIdx.x; i < half; i += TABLE_THREADS) {
     const double turns = rope_freq(d, i) / 6.283185307179586476925;
     per[i] = (unsigned long long)((turns - floor(turns)) * 18446744073709551616.0);
@@ -83,28 +101,15 @@ __global__ void __launch_bounds__(TABLE_THREADS) rope_table_kernel(hq_rope_desc 
   const int row = threadIdx.x / cols;
   if (row >= rows) return;
   for (int i = (threadIdx.x - row * cols); i < sets; i += cols) {
-    uint32_t lo[V], hi[V];
+    unsigned long long f[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      lo[j] = (uint32_t)per[i * V + j];
-      hi[j] = (uint32_t)(per[i * V + j] >> 32);
-    }
+    for (int j = 0; j < V; ++j) f[j] = per[i * V + j];
     const unsigned step = gridDim.x * rows;
     float *to = table + (size_t)(blockIdx.x * rows + row) * d.rot_dim + i * V;
     for (unsigned p = blockIdx.x * rows + row; p < (unsigned)P; p += step, to += (size_t)step * d.rot_dim) {
       float co[V], si[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const uint32_t turn = __umulhi(p, lo[j]) + p * hi[j];  // of 2^32
-        const uint32_t quad = (turn + (1u << 29)) >> 30;
-        const float r = (float)(int)(turn - (quad << 30)) * (6.283185307179586f / 4294967296.f);
-        float s, c;
-        sincos_small(r, s, c);
-        co[j] = amp * ((quad & 1) ? s : c);
-        si[j] = amp * ((quad & 1) ? c : s);
-        if (quad == 1 || quad == 2) co[j] = -co[j];
-        if (quad & 2) si[j] = -si[j];
-      }
+      for (int j = 0; j < V; ++j) turn_cos_sin(f[j] * p, amp, amp_rest, co[j], si[j]);
       if constexpr (V == 4) {
         __stcs(reinterpret_cast<float4 *>(to), make_float4(co[0], co[1], co[2], co[3]));
         __stcs(reinterpret_cast<float4 *>(to + half), make_float4(si[0], si[1], si[2], si[3]));
@@ -121,7 +126,7 @@ hq_status launch_rope_table(const hq_rope_desc *d, int P, float *table, cudaStre
   if (r.amplitude == 0.0) r.amplitude = 1.0;
   const int half = r.rot_dim / 2, v = half % 4 == 0 ? 4 : 1, sets = half / v;
   const int rows = TABLE_THREADS / (sets < TABLE_THREADS ? sets : TABLE_THREADS);
-  const int want = (P + rows - 1) / rows, blocks = want < 148 * 8 ? want : 148 * 8;
+  const int want = (P + rows - 1) / rows, most = 148 * TABLE_BLOCKS, blocks = want < most ? want : most;
   if (v == 4) rope_table_kernel<4><<<blocks, TABLE_THREADS, 0, st>>>(r, P, table);
   else rope_table_kernel<1><<<blocks, TABLE_THREADS, 0, st>>>(r, P, table);
   return check_launch();

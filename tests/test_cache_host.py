@@ -59,6 +59,11 @@ def test_table_arguments():
     hq.hq_rope_table(hq.RopeDesc(**ok), 0, None, stream=0)
 
 
+def test_table_amplitudes():
+    for a in (float("inf"), 1e30):
+        refused(1, hq.hq_rope_table, hq.RopeDesc(rot_dim=64, base=10000.0, amplitude=a), 4, 16)
+
+
 def test_rope_arguments():
     good = dict(T=2, H=2, D=64, x=16, xt=128, xh=64, pos=16, table=16, P=8, out=32, ot=128, oh=64)
 

@@ -124,6 +124,29 @@ def test_table(rot, base, kw, P):
     assert np.max(np.abs(got - want)) <= amp * 4 * 2.0**-23 + P * 2.0**-50
 
 
+@pytest.mark.parametrize("rot,base,kw", [
+    (2, 10000.0, {}), (10, 10000.0, {}), (128, 500000.0, {}), (128, 1e6, dict(scaling=1, factor=32.0)), (256, 1e8, {}),
+    (1024, 10000.0, {}), (128, 10000.0, dict(scaling=3, factor=32.0, context=4096, low=1.0, high=32.0, amplitude=1.3465735902799727)),
+    (96, 1e6, dict(scaling=2, factor=8.0, context=8192, low=1.0, high=4.0, amplitude=1e-3)),
+])
+def test_table_relative_to_each_entry(rot, base, kw):
+    """Small sines, and cosines near a quarter of a turn, have as many bits as the others."""
+    P = 70001
+    t = torch.empty(P, rot, device="cuda")
+    hq.hq_rope_table(hq.RopeDesc(rot_dim=rot, base=base, **kw), P, t)
+    amp = kw.get("amplitude", 1.0)
+    f = freqs64(rot, base, **{k: v for k, v in kw.items() if k != "amplitude"})
+    pos = np.unique(np.concatenate([np.arange(3000), np.linspace(0, P - 1, 3000).astype(np.int64)]))
+    a = np.outer(pos, f)
+    want = amp * np.concatenate([np.cos(a), np.sin(a)], 1)
+    err = np.abs(t.cpu().numpy()[pos].astype(np.float64) - want)
+    # fp32 roundings, each 2^-24 of the entry: of the angle (its low part, the constant, their product), of the sum, of the
+    # product with the amplitude.  The angle: frequencies here and there are off by some 2^-52 of themselves each (a power,
+    # a quotient), the product here by 2^-53, a position by 2^-64 of a turn
+    angle = 2.0**-50 * a + 2.0**-61 * pos[:, None]
+    assert np.all(err <= 5 * 2.0**-24 * np.abs(want) + amp * np.concatenate([angle, angle], 1))
+
+
 def tab64(f, P):
     a = np.outer(np.arange(P), f)
     return torch.from_numpy(np.concatenate([np.cos(a), np.sin(a)], 1)).float()
