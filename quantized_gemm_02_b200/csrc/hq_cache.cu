@@ -126,7 +126,7 @@ hq_status launch_rope_table(const hq_rope_desc *d, int P, float *table, cudaStre
   if (r.amplitude == 0.0) r.amplitude = 1.0;
   const int half = r.rot_dim / 2, v = half % 4 == 0 ? 4 : 1, sets = half / v;
   const int rows = TABLE_THREADS / (sets < TABLE_THREADS ? sets : TABLE_THREADS);
-  const int want = (P + rows - 1) / rows, most = 148 * TABLE_BLOCKS, blocks = want < most ? want : most;
+  const int want = P / rows + (P % rows != 0), most = 148 * TABLE_BLOCKS, blocks = want < most ? want : most;
   if (v == 4) rope_table_kernel<4><<<blocks, TABLE_THREADS, 0, st>>>(r, P, table);
   else rope_table_kernel<1><<<blocks, TABLE_THREADS, 0, st>>>(r, P, table);
   return check_launch();

@@ -147,6 +147,19 @@ def test_table_relative_to_each_entry(rot, base, kw):
     assert np.all(err <= 5 * 2.0**-24 * np.abs(want) + amp * np.concatenate([angle, angle], 1))
 
 
+def test_table_of_the_most_positions():
+    P = 2**31 - 1
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 17 GB")
+    t = torch.full((P, 2), 7.0, device="cuda")
+    hq.hq_rope_table(hq.RopeDesc(rot_dim=2, base=10000.0), P, t)
+    pos = torch.cat([torch.arange(5), torch.linspace(5, P - 1, 1000, dtype=torch.float64).long()]).clamp(max=P - 1)
+    a = pos.double()  # the frequency is 1
+    got = t[pos.cuda()].cpu().double()
+    # as above: 1 / 2 pi is off by 2^-53 of itself and cut to 2^-64, over 2^31 positions
+    assert torch.all((got - torch.stack([a.cos(), a.sin()], 1)).abs() <= 5 * 2.0**-24 + P * 2.0**-53)
+
+
 def tab64(f, P):
     a = np.outer(np.arange(P), f)
     return torch.from_numpy(np.concatenate([np.cos(a), np.sin(a)], 1)).float()
