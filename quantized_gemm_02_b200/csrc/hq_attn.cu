@@ -46,6 +46,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "hq_internal.cuh"
 
 namespace hq {
@@ -1037,13 +1039,13 @@ size_t attn_workspace_bytes(int fmt, int D, int group, int sms) {
 template <int FMT, int D, int NT>
 static hq_status attn_start(const AttnArgs &a, int sms, cudaStream_t st) {
   using S = AttnShape<FMT, D, NT>;
-  static unsigned configured = 0;  // devices whose shared-memory limit is raised
+  static std::atomic<unsigned> configured{0};  // devices whose shared-memory limit is raised
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return HQ_ERR_CUDA;
-  if (dev >= 32 || !(configured & (1u << dev))) {
+  if (dev >= 32 || !(configured.load(std::memory_order_acquire) & (1u << dev))) {
     if (cudaFuncSetAttribute(attn_kernel<FMT, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) != cudaSuccess)
       return HQ_ERR_CUDA;
-    if (dev < 32) configured |= 1u << dev;
+    if (dev < 32) configured.fetch_or(1u << dev, std::memory_order_release);
   }
   attn_kernel<FMT, D, NT><<<sms, (S::W + S::P) * 32, S::SMEM, st>>>(a);
   return check_launch();

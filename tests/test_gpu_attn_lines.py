@@ -3,6 +3,7 @@
 The units of all sequences and kv heads form one line that is cut over some 450 to 2100 warps; the cases here are
 longer than that, so that warps go from page to page, from item to item and around their rings."""
 import math
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 import torch
@@ -223,3 +224,27 @@ def test_scores_that_grow(dtype, D, G):
     q = normal((len(lens), 4 * G, D), 63, 1.0)
     q[:, ::2, 0], q[:, 1::2, 0] = 600.0, -600.0
     c.check(q, 0.125)
+
+
+def test_calls_from_several_threads():
+    """Each thread with a stream and a workspace of its own; in a fresh process these are first calls of their kernels."""
+    c = [Paged("e4m3", 2, 192, 48, [700, 0, 33, 1200], [0] * 4, 71), Paged("bf16", 1, 256, 16, [900, 5], [0] * 2, 72)]
+    q = [normal((len(x.lens), x.H * 9, x.D), 73) for x in c]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(8)]
+
+    def one(i):
+        x, s = c[i % 2], streams[i]
+        with torch.cuda.stream(s):
+            got = [x.call(q[i % 2], 0.07) for _ in range(5)]
+        s.synchronize()
+        return got
+
+    with ThreadPoolExecutor(8) as pool:
+        got = list(pool.map(one, range(8)))
+    assert hq.hq_device_error() == 0
+    for i in range(2):
+        c[i].check(q[i], 0.07)
+        want = c[i].call(q[i], 0.07)
+        for runs in got[i::2]:
+            assert all(torch.equal(a, b) for r in runs for a, b in zip(r, want))
