@@ -349,43 +349,43 @@ def hq_moe_gemm_gated(mode, desc, T, topk, E, I, K, packed_w, a, a_scales, a_glo
         _ptr(topk_ids), _ptr(expert_offsets), _ptr(perm), _ptr(out), _ptr(workspace), ws_bytes, _stream(stream)))
 
 
-def _on_device(fn, *tensors):
-    """Device pointers of tensors (None and integer addresses pass): each has
-    to be on the current CUDA device, whose stream the call runs on."""
+_KINDS = None
+
+
+def _on_device(fn, kinds, *tensors):
+    """Device pointers of tensors (None and integer addresses pass).  Each has
+    to be on the current CUDA device, whose stream the call runs on, and to
+    hold what the kernels take it for, or they would read or write past its
+    end: b bf16 (or its bits as 16-bit integers), f fp32, i int32, l int64
+    (f, i and l contiguous), - any."""
+    global _KINDS
     dev, out = None, []
-    for t in tensors:
+    for kind, t in zip(kinds, tensors):
         if t is None or isinstance(t, int):
             out.append(t)
             continue
+        if _KINDS is None:
+            T = _cuda()
+            _KINDS = {"b": (T.bfloat16, T.int16, T.uint16), "f": (T.float32,), "i": (T.int32,), "l": (T.int64,)}
         d = t.get_device()
         if dev is None and d >= 0:
             dev = _cuda().cuda.current_device()
-        if d < 0 or d != dev:
+        if d < 0 or d != dev or (kind != "-" and (t.dtype not in _KINDS[kind] or (kind != "b" and not t.is_contiguous()))):
             raise HQError(fn, 1)
         out.append(t.data_ptr())
     return out
 
 
-def _indices(fn, wide, *tensors):
-    """Index tensors of another integer width would be read past their end:
-    int64 (wide) or int32, contiguous."""
-    for t in tensors:
-        if t is not None and not isinstance(t, int) and (t.dtype != (_cuda().int64 if wide else _cuda().int32)
-                                                         or not t.is_contiguous()):
-            raise HQError(fn, 1)
-
-
 def hq_rope_table(rope, P, table, stream=None):
     """Cosines and sines of P positions, fp32 [P, rope.rot_dim]."""
-    table, = _on_device("hq_rope_table", table)
+    table, = _on_device("hq_rope_table", "f", table)
     _check("hq_rope_table", _lib().hq_rope_table(ctypes.byref(rope), P, table, _stream(stream)))
 
 
 def hq_rope(rope, T, H, D, x, x_token_stride, x_head_stride, positions, table, P, out, out_token_stride,
             out_head_stride, stream=None):
     """Rotates x [T, H, D] by the positions' rows of `table` into out (which may be x)."""
-    _indices("hq_rope", False, positions)
-    x, positions, table, out = _on_device("hq_rope", x, positions, table, out)
+    x, positions, table, out = _on_device("hq_rope", "bifb", x, positions, table, out)
     _check("hq_rope", _lib().hq_rope(
         ctypes.byref(rope), T, H, D, x, x_token_stride, x_head_stride, positions, table, P, out, out_token_stride,
         out_head_stride, _stream(stream)))
@@ -397,8 +397,7 @@ def hq_kv_page_bytes(kv) -> int:
 
 def hq_kv_write(kv, T, k, k_stride, v, v_stride, slots, global_scale, num_pages, pages, stream=None):
     """Quantises T tokens' keys and values into their slots of the paged cache."""
-    _indices("hq_kv_write", True, slots)
-    k, v, slots, global_scale, pages = _on_device("hq_kv_write", k, v, slots, global_scale, pages)
+    k, v, slots, global_scale, pages = _on_device("hq_kv_write", "bblf-", k, v, slots, global_scale, pages)
     _check("hq_kv_write", _lib().hq_kv_write(
         ctypes.byref(kv), T, k, k_stride, v, v_stride, slots, global_scale, num_pages, pages, _stream(stream)))
 
@@ -406,10 +405,8 @@ def hq_kv_write(kv, T, k, k_stride, v, v_stride, slots, global_scale, num_pages,
 def hq_rope_kv_write(rope, kv, T, q_heads, q, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride, positions,
                      table, P, slots, global_scale, num_pages, pages, stream=None):
     """hq_kv_write with k (and q, into q_out) rotated, in one launch."""
-    _indices("hq_rope_kv_write", True, slots)
-    _indices("hq_rope_kv_write", False, positions)
     q, q_out, k, v, positions, table, slots, global_scale, pages = _on_device(
-        "hq_rope_kv_write", q, q_out, k, v, positions, table, slots, global_scale, pages)
+        "hq_rope_kv_write", "bbbbiflf-", q, q_out, k, v, positions, table, slots, global_scale, pages)
     _check("hq_rope_kv_write", _lib().hq_rope_kv_write(
         ctypes.byref(rope), ctypes.byref(kv), T, q_heads, q, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride,
         positions, table, P, slots, global_scale, num_pages, pages, _stream(stream)))
@@ -417,8 +414,8 @@ def hq_rope_kv_write(rope, kv, T, q_heads, q, q_stride, q_out, q_out_stride, k, 
 
 def hq_kv_read(kv, T, slots, global_scale, num_pages, pages, k_out, k_stride, v_out, v_stride, stream=None):
     """Reads T slots of the paged cache back to bf16."""
-    _indices("hq_kv_read", True, slots)
-    slots, global_scale, pages, k_out, v_out = _on_device("hq_kv_read", slots, global_scale, pages, k_out, v_out)
+    slots, global_scale, pages, k_out, v_out = _on_device("hq_kv_read", "lf-bb", slots, global_scale, pages, k_out,
+                                                          v_out)
     _check("hq_kv_read", _lib().hq_kv_read(
         ctypes.byref(kv), T, slots, global_scale, num_pages, pages, k_out, k_stride, v_out, v_stride,
         _stream(stream)))
@@ -431,9 +428,8 @@ def hq_paged_attn_workspace_bytes(kv, B, q_heads) -> int:
 def hq_paged_attn(kv, B, q_heads, q, q_stride, global_scale, num_pages, pages, page_table, max_pages, lengths, scale,
                   window, out, out_stride, lse, workspace, ws_bytes, stream=None):
     """Attention of one new token per sequence over the paged cache."""
-    _indices("hq_paged_attn", False, page_table, lengths)
     q, global_scale, pages, page_table, lengths, out, lse, workspace = _on_device(
-        "hq_paged_attn", q, global_scale, pages, page_table, lengths, out, lse, workspace)
+        "hq_paged_attn", "bf-iibf-", q, global_scale, pages, page_table, lengths, out, lse, workspace)
     _check("hq_paged_attn", _lib().hq_paged_attn(
         ctypes.byref(kv), B, q_heads, q, q_stride, global_scale, num_pages, pages, page_table, max_pages, lengths,
         scale, window, out, out_stride, lse, workspace, ws_bytes, _stream(stream)))

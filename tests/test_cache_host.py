@@ -148,3 +148,49 @@ def test_index_tensors_of_another_width_are_refused():
     refused(1, hq.hq_paged_attn, OK, 1, 8, 16, 1024, None, 4, 16, 16, 4, i64, 1.0, 0, 16, 1024, None, 16, need)
     refused(1, hq.hq_paged_attn, OK, 1, 8, 16, 1024, None, 4, 16, torch.zeros(2, 4, dtype=torch.int32).t(), 4, 16, 1.0, 0, 16,
             1024, None, 16, need)
+
+
+class OnDevice:
+    """A host tensor that says it is on the current device (nothing is launched here: no tokens, no sequences)."""
+    def __init__(self, t):
+        self.t, self.dtype = t, t.dtype
+
+    def get_device(self):
+        return 0
+
+    def data_ptr(self):
+        return 4096
+
+    def is_contiguous(self):
+        return self.t.is_contiguous()
+
+
+def test_tensors_of_another_type_are_refused(monkeypatch):
+    """An lse or a table of 16 bits would be written past its end, rows of 16 other bits would be misread."""
+    import torch
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    t = lambda dtype, *shape: OnDevice(torch.zeros(shape or (4,), dtype=dtype))  # noqa: E731
+    bf, f32, f16, f64, i32, i64, u8 = (t(x) for x in (torch.bfloat16, torch.float32, torch.float16, torch.float64, torch.int32,
+                                                      torch.int64, torch.uint8))
+    strided = OnDevice(torch.zeros(4, 8)[:, ::2])
+    rope = hq.RopeDesc(rot_dim=64, base=10000.0)
+    nv = kv(dtype=hq.HQ_NVFP4)
+
+    def both(fn, good, *bad):
+        fn(*good, stream=0)
+        for at, x in bad:
+            args = list(good)
+            args[at] = x
+            refused(1, fn, *args)
+
+    both(hq.hq_rope_table, (rope, 0, f32), (2, f16), (2, f64), (2, bf), (2, strided))
+    both(hq.hq_rope, (rope, 0, 1, 64, bf, 64, 64, i32, f32, 4, bf, 64, 64), (4, f16), (4, f32), (10, f16), (8, f16), (8, f64),
+         (7, i64), (8, strided))
+    both(hq.hq_kv_write, (nv, 0, bf, 1024, bf, 1024, i64, f32, 4, u8), (2, f16), (4, f32), (6, i32), (7, bf), (7, f64))
+    both(hq.hq_rope_kv_write, (rope, nv, 0, 8, bf, 1024, bf, 1024, bf, 1024, bf, 1024, i32, f32, 4, i64, f32, 4, u8), (4, f16),
+         (6, f32), (8, f16), (10, f16), (12, i64), (13, f16), (15, i32), (16, f16))
+    both(hq.hq_kv_read, (nv, 0, i64, f32, 4, u8, bf, 1024, bf, 1024), (2, i32), (3, f64), (6, f16), (8, f32))
+    both(hq.hq_paged_attn, (nv, 0, 32, bf, 4096, f32, 4, u8, i32, 4, i32, 1.0, 0, bf, 4096, f32, u8, 1 << 30), (3, f16), (5, f16),
+         (8, i64), (10, i64), (13, f32), (15, f16), (15, f64), (15, strided))
+    bits = t(torch.int16)  # the bits of bf16 pass, as elsewhere in the library
+    hq.hq_rope(rope, 0, 1, 64, bits, 64, 64, i32, f32, 4, bits, 64, 64, stream=0)
