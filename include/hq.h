@@ -511,7 +511,7 @@ HQ_API hq_status hq_rope(const hq_rope_desc *rope, int T, int H, int D, const vo
  * the whole description.  What is held, per token and head:
  *   HQ_BF16   the bf16 values
  *   HQ_E4M3   E4M3 codes and one fp32 scale: hq_quant_act's per-token recipe
- *             on the head's channels (s = amax / 448, 1 for an all-zero row)
+ *             on the head's channels (s = amax / 448, 1 where that is 0)
  *   HQ_NVFP4  E2M1 codes and a UE4M3 scale per 16 channels under a static
  *             second-level scale: hq_quant_act's recipe with static_global;
  *             global_scale is device fp32 [2], for K and for V, each > 0,

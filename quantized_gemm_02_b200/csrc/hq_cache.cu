@@ -532,7 +532,11 @@ __device__ __forceinline__ float amax8(const float *f) {
   return m;
 }
 // hq_quant_act's per-token recipe on a head's D channels
-__device__ __forceinline__ float e4m3_scale(float amax) { return (amax == 0.f) ? 1.f : __fdiv_rn(amax, 448.f); }
+// (rotated channels reach below bf16's smallest number, where the quotient may be 0)
+__device__ __forceinline__ float e4m3_scale(float amax) {
+  const float s = __fdiv_rn(amax, 448.f);
+  return s == 0.f ? 1.f : s;
+}
 // Correctly rounded quotients by one divisor, by Markstein's theorem ("Computation
 // of elementary functions on the IBM RISC System/6000 processor", 1990): with
 // y the correctly rounded 1 / d and q within one step of x / d, r = x - q d is

@@ -420,6 +420,27 @@ def test_rope_kv_write(dtype, inter, D, rot, Hq, in_place):
         assert np.all(err <= 2.0**-8 * np.abs(want) + 2.0**-21 * 8)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "nvfp4"])
+def test_rope_kv_write_of_rows_next_to_nothing(dtype):
+    """bf16's smallest numbers under a table of small amplitude: finite values, as small as the rows."""
+    H, T, D, P = 2, 20, 128, 8
+    c = Cache(dtype, H, D, 16, 2)
+    k = (normal((T, H, D), 31).float().sign() * 2.0**-133).to(torch.bfloat16)
+    v = normal((T, H, D), 32)
+    table = (tab64(freqs64(128, 10000.0), P) * torch.exp2(-torch.arange(P).float())[:, None]).cuda()  # to 2^-7
+    table[4:] *= 2.0**-8
+    pos, slots = torch.arange(T, dtype=torch.int32) % P, torch.arange(T)
+    kd, vd = k.cuda(), v.cuda()
+    hq.hq_rope_kv_write(hq.RopeDesc(rot_dim=128), c.kv, T, 0, None, 0, None, 0, kd, kd.stride(0), vd, vd.stride(0), pos.cuda(),
+                        table, P, slots.cuda(), c.glob, 2, c.buf)
+    rk, rv = c.read(slots)
+    assert hq.hq_device_error() == 0
+    # |a c - b s| <= sqrt(2) 2^-133; what is held is off by no more than the largest channel
+    assert torch.all(rk.double().abs() <= 2.0**-132)
+    want, _ = expected_read(v, dtype, GLOB[1])
+    assert torch.equal(rv, want)
+
+
 # ---- attention ----------------------------------------------------------------
 
 def attn64(q, k, v, first, n, scale, group):
