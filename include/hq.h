@@ -561,7 +561,7 @@ HQ_API hq_status hq_kv_read(const hq_kv_desc *kv, int T, const int64_t *slots, c
  * written); its token j is token j % page_size of page
  * page_table[b, j / page_size] (device int32 [B, max_pages]; entries past the
  * length are not read).  Query head i uses kv head i / (q_heads / heads);
- * q_heads is a multiple of heads.  With x_j = scale * q . k_j over
+ * q_heads is a multiple of heads; |scale| <= 2e38.  With x_j = scale * q . k_j over
  * max(0, length - window) <= j < length (window 0: all of them),
  *   out[b, i] = sum_j exp(x_j) v_j / sum_j exp(x_j)   bf16 [B, q_heads, head_dim]
  *   lse[b, i] = ln sum_j exp(x_j)                     fp32 [B, q_heads], may be NULL

@@ -884,7 +884,7 @@ hq_status hq_paged_attn(const hq_kv_desc *kv, int B, int q_heads, const void *q_
       !valid_out_stride(out_stride, B, (int64_t)q_heads * kv->head_dim) || max_pages < 1 ||
       (int64_t)max_pages * kv->page_size > (1 << 30) || window < 0)
     return HQ_ERR_INVALID_ARG;
-  if (!(scale >= -3e38f && scale <= 3e38f)) return HQ_ERR_INVALID_ARG;
+  if (!(scale >= -2e38f && scale <= 2e38f)) return HQ_ERR_INVALID_ARG;  // the kernel's is 1.44 times that
   if (B == 0) return HQ_OK;
   if (!q_bf16 || !page_table || !lengths || !out_bf16 || !aligned16(q_bf16) || !aligned16(out_bf16) ||
       !aligned_to(page_table, 4) || !aligned_to(lengths, 4) || !aligned_to(lse, 4))

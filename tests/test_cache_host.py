@@ -132,6 +132,12 @@ def test_attention_arguments():
     assert hq.hq_paged_attn_workspace_bytes(OK, 4, 33) == 0
 
 
+def test_attention_scales_that_overflow_in_base_2():
+    need = hq.hq_paged_attn_workspace_bytes(OK, 1, 8)
+    for scale in (2.5e38, -3e38):
+        refused(1, hq.hq_paged_attn, OK, 1, 8, 16, 1024, None, 4, 16, 16, 4, 16, scale, 0, 16, 1024, None, 16, need)
+
+
 def test_tensors_that_are_not_on_the_device_are_refused():
     import torch
     t = torch.zeros(4, 64)
