@@ -569,9 +569,12 @@ HQ_API hq_status hq_kv_read(const hq_kv_desc *kv, int T, const int64_t *slots, c
  * max_pages * page_size (at most 2^30) sets HQ_ERR_DEVICE_INDEX and counts as
  * 0 or as that bound; a page id outside the cache sets it too and its tokens
  * are left out.  Slots past a length and pages before the window may hold
- * anything.  Scores, softmax and sums are fp32; the result does not depend on
- * timing.  From 2^34 tokens times kv heads on (each once per 16 query heads) a
- * call may set HQ_ERR_UNSUPPORTED in the device error word and then writes
+ * anything.  Scores, softmax and sums are fp32; the weights exp(x_j) that meet
+ * v_j are fp32 over a BF16 cache and rounded to fp16 (2^-11 of each) over the
+ * others.  The result does not depend on timing.  Blocks of 16 tokens, counted
+ * from a sequence's start, that attended tokens lie in, times kv heads, times
+ * ceil(query heads per kv head / 16): from a sum of 2^30 on a call may set
+ * HQ_ERR_UNSUPPORTED in the device error word and then writes
  * nothing but the rows of empty sequences.  `workspace` as for hq_gemm: of
  * hq_paged_attn_workspace_bytes() bytes, its counters zero when first used and
  * left zero by every completed call (after HQ_ERR_TIMEOUT, zero them again);

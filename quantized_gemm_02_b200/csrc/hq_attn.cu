@@ -36,11 +36,16 @@
 // the join is 1 to 2 us).
 //
 // Arithmetic.  Scores and sums are fp32.  bf16 caches multiply in bf16 with
-// each weight split into two bf16 numbers (hi + lo, 2^-17 of the weight);
-// E4M3 and NVFP4 codes (and code times block scale) are exact in fp16, so
-// those caches multiply in fp16, with q scaled by a power of two per head into
-// fp16's range (exact down to 2^-39 of the head's largest) and weights rounded
-// to fp16 (2^-11) around a reference of 2^10.  E4M3 values carry an fp32 scale
+// each weight split into three bf16 numbers, together its 24 bits (two, 2^-17
+// of it, were 0 to 1% faster, 3% with 16 heads of 256 channels).  E4M3 and NVFP4
+// codes (and code times block scale) are exact in fp16, so those caches multiply in fp16, with q scaled by
+// a power of two per head into fp16's range (exact down to 2^-39 of the head's
+// largest) and weights rounded to fp16 around a reference of 2^10.  That is
+// 2^-11 of a weight, under a hundredth of the step of what is held (two fp16
+// numbers, 2^-22: E4M3 64 ragged x 8192 64.8 -> 65.8 us, 33 ragged x 16384 with
+// wide heads 82.6 -> 87.2, NVFP4 8 x 107000 229 -> 250, and bf16 results 0.0001
+// to 0.0002 of their norm from those of fp32 weights instead of 0.0007 to
+// 0.0008, where their own rounding is 0.0017).  E4M3 values carry an fp32 scale
 // per token: it multiplies the weight, and those products have a reference of
 // their own, so that any range of scales keeps the weight's precision.
 #include <cuda_bf16.h>
@@ -701,7 +706,8 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
               }
             }
         }
-        uint32_t pb[NT][STEP][2], pl[NT][STEP][2];  // B fragments of P^T: tokens 2t, 2t + 1 (+ 8), head g
+        constexpr int PARTS = BF ? 3 : 1;  // summands of a weight, each what the ones before lack
+        uint32_t pb[NT][STEP][PARTS][2];   // B fragments of P^T: tokens 2t, 2t + 1 (+ 8), head g
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -716,12 +722,13 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
             l[nt][1] += p[1] + p[3];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              if constexpr (BF) {
-                const uint32_t hi2 = bf16x2(w[2 * r], w[2 * r + 1]);
-                pb[nt][k][r] = transpose8(hi2);
-                pl[nt][k][r] = transpose8(bf16x2(w[2 * r] - bf16_lo(hi2), w[2 * r + 1] - bf16_hi(hi2)));
-              } else {
-                pb[nt][k][r] = transpose8(f16x2(w[2 * r], w[2 * r + 1]));
+              float w0 = w[2 * r], w1 = w[2 * r + 1];
+#pragma unroll
+              for (int i = 0; i < PARTS; ++i) {
+                const uint32_t h = BF ? bf16x2(w0, w1) : f16x2(w0, w1);
+                pb[nt][k][i][r] = transpose8(h);
+                w0 -= bf16_lo(h);
+                w1 -= bf16_hi(h);
               }
             }
           }
@@ -733,8 +740,8 @@ __global__ void __launch_bounds__(AttnShape<FMT, D, NT>::W * 32 + AttnShape<FMT,
           auto pv = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma16816<BF>(o[nt][i], a0, a1, a2, a3, pb[nt][k][0], pb[nt][k][1]);
-              if constexpr (BF) mma16816<BF>(o[nt][i], a0, a1, a2, a3, pl[nt][k][0], pl[nt][k][1]);
+#pragma unroll
+              for (int j = 0; j < PARTS; ++j) mma16816<BF>(o[nt][i], a0, a1, a2, a3, pb[nt][k][j][0], pb[nt][k][j][1]);
             }
           };
 #pragma unroll

@@ -226,6 +226,31 @@ def test_scores_that_grow(dtype, D, G):
     c.check(q, 0.125)
 
 
+def test_bf16_weights_keep_their_bits():
+    """Two tokens of nearly equal weight and opposite values, beside one that the softmax refers to: what is left is
+    2^-15 of the weights, so that a weight in fewer bits shows."""
+    B = 512
+
+    def make(seqs, toks):
+        k = torch.zeros(3 * B, 1, 64, dtype=torch.bfloat16, device="cuda")
+        k[:, 0, 0] = torch.tensor([1.0, 1.0078125, 0.0], device="cuda")[toks].to(torch.bfloat16)
+        k[2::3, 0, 1] = 1.0
+        v = torch.zeros_like(k)
+        v[0::3], v[1::3] = 1.0, -1.0
+        return k, v
+
+    c = Paged("bf16", 1, 64, 16, [3] * B, [0] * B, 81, make)
+    q = torch.zeros(B, 8, 64, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0 + normal((B, 8), 82).abs().clamp(max=2.0)
+    q[..., 1] = 40.0 + 30.0 * normal((B, 8), 83).abs().clamp(max=4.0)
+    out, _ = c.call(q, 0.01)
+    x = 0.01 * torch.einsum("bgd,jd->bgj", q.double(), c.k[:3, 0].double())
+    p = torch.softmax(x, -1)
+    want, mag = (p[..., 0] - p[..., 1])[..., None], (p[..., 0] + p[..., 1])[..., None]
+    # exp2 is off by 2^-22, its argument (up to 4) by 2^-23; both of two weights, and some 2^-24 of sums: under 2^-20
+    assert torch.all((out.double() - want).abs() <= 2.0**-8 * want.abs() + 2.0**-20 * mag)
+
+
 def test_calls_from_several_threads():
     """Each thread with a stream and a workspace of its own; in a fresh process these are first calls of their kernels."""
     c = [Paged("e4m3", 2, 192, 48, [700, 0, 33, 1200], [0] * 4, 71), Paged("bf16", 1, 256, 16, [900, 5], [0] * 2, 72)]
