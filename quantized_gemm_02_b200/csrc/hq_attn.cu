@@ -37,17 +37,18 @@
 //
 // Arithmetic.  Scores and sums are fp32.  bf16 caches multiply in bf16 with
 // each weight split into three bf16 numbers, together its 24 bits (two, 2^-17
-// of it, were 0 to 1% faster, 3% with 16 heads of 256 channels).  E4M3 and NVFP4
-// codes (and code times block scale) are exact in fp16, so those caches multiply in fp16, with q scaled by
-// a power of two per head into fp16's range (exact down to 2^-39 of the head's
-// largest) and weights rounded to fp16 around a reference of 2^10.  That is
-// 2^-11 of a weight, under a hundredth of the step of what is held (two fp16
-// numbers, 2^-22: E4M3 64 ragged x 8192 64.8 -> 65.8 us, 33 ragged x 16384 with
-// wide heads 82.6 -> 87.2, NVFP4 8 x 107000 229 -> 250, and bf16 results 0.0001
-// to 0.0002 of their norm from those of fp32 weights instead of 0.0007 to
-// 0.0008, where their own rounding is 0.0017).  E4M3 values carry an fp32 scale
-// per token: it multiplies the weight, and those products have a reference of
-// their own, so that any range of scales keeps the weight's precision.
+// of it, were 0 to 1% faster, 3% with 16 heads of 256 channels).  E4M3 and
+// NVFP4 codes (and code times block scale) are exact in fp16, so those caches
+// multiply in fp16, with q scaled by a power of two per head into fp16's range
+// (exact down to 2^-39 of the head's largest) and weights rounded to fp16
+// around a reference of 2^10.  That is 2^-11 of a weight, under a hundredth of
+// the step of what is held (two fp16 numbers, 2^-22: E4M3 64 ragged x 8192
+// 64.8 -> 65.8 us, 33 ragged x 16384 with wide heads 82.6 -> 87.2, NVFP4 8 x
+// 107000 229 -> 250, and bf16 results 0.0001 to 0.0002 of their norm from those
+// of fp32 weights instead of 0.0007 to 0.0008, where their own rounding is
+// 0.0017).  E4M3 values carry an fp32 scale per token: it multiplies the weight,
+// and those products have a reference of their own, so that any range of scales
+// keeps the weight's precision.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -273,3 +273,71 @@ def test_calls_from_several_threads():
         want = c[i].call(q[i], 0.07)
         for runs in got[i::2]:
             assert all(torch.equal(a, b) for r in runs for a, b in zip(r, want))
+
+
+def test_the_most_sequences():
+    """2^20 sequences of 0 to 3 tokens on shared pages: thousands of lengths a thread of the scan."""
+    B, D, pages = 1 << 20, 64, 4096
+    kv = hq.KVDesc(dtype=hq.HQ_BF16, heads=1, head_dim=D, page_size=16)
+    buf = torch.full((pages * hq.hq_kv_page_bytes(kv),), 0xFF, dtype=torch.uint8, device="cuda")
+    k, v = normal((pages * 3, 1, D), 91), normal((pages * 3, 1, D), 92)
+    at = torch.arange(pages * 3, device="cuda")
+    hq.hq_kv_write(kv, pages * 3, k, D, v, D, at // 3 * 16 + at % 3, None, pages, buf)
+    page = torch.randint(0, pages, (B, 1), generator=gen(93), device="cuda", dtype=torch.int32)
+    lens = torch.randint(0, 4, (B,), generator=gen(94), device="cuda", dtype=torch.int32)
+    lens[-5000:] = 0
+    q = normal((B, 1, D), 95)
+    out, lse = torch.full_like(q, 7.0), torch.full((B, 1), 7.0, device="cuda")
+    ws = torch.zeros(hq.hq_paged_attn_workspace_bytes(kv, B, 1), dtype=torch.uint8, device="cuda")
+    hq.hq_paged_attn(kv, B, 1, q, D, None, pages, buf, page, 1, lens, 0.125, 0, out, D, lse, ws, ws.numel())
+    assert hq.hq_device_error() == 0
+    rows = page.long() * 3 + torch.arange(3, device="cuda")
+    kk, vv = k[rows, 0].double(), v[rows, 0].double()
+    x = 0.125 * torch.einsum("bd,bjd->bj", q[:, 0].double(), kk)
+    x = torch.where(torch.arange(3, device="cuda") < lens[:, None], x, -math.inf)
+    wl = torch.logsumexp(x, -1)
+    p = torch.exp(x - wl[:, None]).nan_to_num(nan=0.0)
+    want, mag = torch.einsum("bj,bjd->bd", p, vv), torch.einsum("bj,bjd->bd", p, vv.abs())
+    dx = 2.0**-18 * 0.125 * torch.einsum("bd,bjd->bj", q[:, 0].double().abs(), kk.abs()).amax(-1)
+    assert torch.all((out[:, 0].double() - want).abs() <= 2.0**-8 * want.abs() + (2.0**-10 + 2 * dx[:, None]) * mag)
+    some = lens > 0
+    assert torch.all((lse[:, 0].double() - wl).abs()[some] <= (2.0**-20 * (1 + wl.abs()) + dx)[some])
+    assert torch.all(lse[~some] == -math.inf)
+
+
+@pytest.mark.parametrize("dtype,H,D,page", [("bf16", 1024, 64, 16), ("e4m3", 1024, 64, 32), ("nvfp4", 512, 128, 4096)])
+def test_the_most_heads_and_the_largest_pages(dtype, H, D, page):
+    lens = [40, 0, 1, 333]
+    c = Paged(dtype, H, D, page, lens, [0] * 4, 101)
+    c.check(normal((4, H, D), 102), 0.1)
+
+
+@pytest.mark.parametrize("dtype,D,page", [("bf16", 256, 64), ("e4m3", 128, 256), ("nvfp4", 192, 16)])
+def test_a_cache_past_32_bits(dtype, D, page):
+    """Tokens in the first and the last pages of a cache of more than 4 GB."""
+    H, n = 8, 300
+    kv = hq.KVDesc(dtype=DT[dtype], heads=H, head_dim=D, page_size=page)
+    size = hq.hq_kv_page_bytes(kv)
+    pages = (9 << 29) // size
+    buf = torch.empty(pages * size, dtype=torch.uint8, device="cuda")
+    glob = torch.tensor(GLOB, device="cuda") if dtype == "nvfp4" else None
+    need = -(-n // page)
+    table = torch.stack([torch.arange(need), pages - 1 - torch.arange(need)]).to(torch.int32)
+    slots = (table.long()[:, torch.arange(n) // page] * page + torch.arange(n) % page).reshape(-1).cuda()
+    k, v = normal((2 * n, H, D), 111), normal((2 * n, H, D), 112)
+    hq.hq_kv_write(kv, 2 * n, k, H * D, v, H * D, slots, glob, pages, buf)
+    back = [torch.empty_like(k) for _ in range(2)]
+    hq.hq_kv_read(kv, 2 * n, slots, glob, pages, buf, back[0], H * D, back[1], H * D)
+    for got, x, g in zip(back, (k, v), GLOB):
+        assert torch.equal(got, held64(x, dtype, g).float().to(torch.bfloat16))
+    q = normal((2, 4 * H, D), 113)
+    ws = torch.zeros(hq.hq_paged_attn_workspace_bytes(kv, 2, 4 * H), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(2, 4 * H, device="cuda")
+    lens = torch.full((2,), n, dtype=torch.int32, device="cuda")
+    hq.hq_paged_attn(kv, 2, 4 * H, q, q.stride(0), glob, pages, buf, table.cuda(), need, lens, 0.1, 0, out, out.stride(0), lse, ws,
+                     ws.numel())
+    assert hq.hq_device_error() == 0
+    small = Paged(dtype, H, D, page, [n, n], [0, 0], 114, lambda seqs, toks: (k, v))  # the same tokens on few pages
+    want = small.call(q, 0.1)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    small.check(q, 0.1)
