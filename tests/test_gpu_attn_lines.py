@@ -341,3 +341,120 @@ def test_a_cache_past_32_bits(dtype, D, page):
     want = small.call(q, 0.1)
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
     small.check(q, 0.1)
+
+
+# ---- prompts and captured steps: what surrounds the attention --------------------
+
+def turned(x, pos, table, rot, inter):
+    """The rotation in the entry points' fp32 steps (separate torch operations: nothing is fused)."""
+    t = table[pos.long()][:, None]
+    co, si = t[..., :rot // 2], t[..., rot // 2:]
+    x = x.float()
+    a, b = (x[..., :rot:2], x[..., 1:rot:2]) if inter else (x[..., :rot // 2], x[..., rot // 2:rot])
+    a, b = a * co - b * si, b * co + a * si
+    y = x.clone()
+    y[..., :rot] = torch.stack([a, b], -1).flatten(-2) if inter else torch.cat([a, b], -1)
+    return y
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("D,rot,inter,Hq", [(64, 64, 0, 5), (128, 128, 0, 8), (128, 40, 1, 3), (192, 64, 1, 16), (192, 136, 0, 0),
+                                            (256, 256, 1, 1), (256, 136, 1, 7), (256, 18, 0, 12), (128, 0, 0, 0)])
+def test_prompts(dtype, D, rot, inter, Hq):
+    """A prompt of 3001 tokens on pages in any order, its tail padded: every held value and every q is the recipe's."""
+    T, H, page, P = 3001, 3, 48, 5000
+    pages = -(-T // page) + 1
+    kv = hq.KVDesc(dtype=DT[dtype], heads=H, head_dim=D, page_size=page)
+    glob = torch.tensor(GLOB, device="cuda") if dtype == "nvfp4" else None
+    buf = torch.full((pages * hq.hq_kv_page_bytes(kv),), 0xA5, dtype=torch.uint8, device="cuda")
+    qkv = normal((T, Hq + 2 * H, D), 121)
+    q, k, v = qkv.split([Hq, H, H], 1)
+    at = torch.arange(T, device="cuda") + 7
+    slots = torch.randperm(pages, generator=gen(122), device="cuda")[at // page] * page + at % page
+    slots[-9:] = -1
+    row = qkv.stride(0)
+    if rot:
+        a = torch.outer(torch.arange(P, device="cuda").double(), 10000.0 ** (-2.0 * torch.arange(rot // 2, device="cuda").double() / rot))
+        table = torch.cat([a.cos(), a.sin()], 1).float()
+        pos = torch.randint(0, P, (T,), generator=gen(123), device="cuda", dtype=torch.int32)
+        qo = torch.empty(T, Hq, D, dtype=torch.bfloat16, device="cuda") if Hq else None
+        hq.hq_rope_kv_write(hq.RopeDesc(rot_dim=rot, interleaved=inter), kv, T, Hq, q if Hq else None, row, qo, Hq * D, k, row, v,
+                            row, pos, table, P, slots, glob, pages, buf)
+        kx = turned(k, pos, table, rot, inter)
+        if Hq:
+            assert torch.equal(qo, turned(q, pos, table, rot, inter).to(torch.bfloat16))
+    else:
+        hq.hq_kv_write(kv, T, k, row, v, row, slots, glob, pages, buf)
+        kx = k.float()
+    back = [torch.full((T, H, D), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    hq.hq_kv_read(kv, T, slots, glob, pages, buf, back[0], H * D, back[1], H * D)
+    assert hq.hq_device_error() == 0
+    for got, x, g in zip(back, (kx, v.float()), GLOB):
+        want = (x.to(torch.bfloat16) if dtype == "bf16" else held64(x, dtype, g).float().to(torch.bfloat16))
+        want[-9:] = 3.0
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("e4m3", 192), ("nvfp4", 128)])
+def test_a_captured_step_follows_its_sequences(dtype, D):
+    """Rotation, write and attention in one graph; positions, slots, lengths and the projection's output change between
+    replays.  The result is that of the same calls outside a graph, and attends what the steps have written."""
+    B, H, G, page, P, window = 5, 2, 6, 64, 512, 40
+    kv = hq.KVDesc(dtype=DT[dtype], heads=H, head_dim=D, page_size=page)
+    glob = torch.tensor(GLOB, device="cuda") if dtype == "nvfp4" else None
+    rope, table = hq.RopeDesc(rot_dim=D, base=10000.0), torch.empty(P, D, device="cuda")
+    hq.hq_rope_table(rope, P, table)
+    most, pages = 3, 16
+    pt = torch.randperm(pages - 1, generator=gen(131), device="cuda")[:B * most].to(torch.int32).reshape(B, most)
+    steps = [normal((B, H * (G + 2), D), 140 + s) for s in range(130)]
+
+    def program():
+        z = lambda *s, dtype: torch.zeros(*s, dtype=dtype, device="cuda")  # noqa: E731
+        s = dict(buf=torch.full((pages * hq.hq_kv_page_bytes(kv),), 0xFF, dtype=torch.uint8, device="cuda"),
+                 qkv=torch.zeros_like(steps[0]), pos=z(B, dtype=torch.int32), slots=z(B, dtype=torch.int64),
+                 lens=z(B, dtype=torch.int32), q=z(B, H * G, D, dtype=torch.bfloat16), out=z(B, H * G, D, dtype=torch.bfloat16),
+                 lse=z(B, H * G, dtype=torch.float32),
+                 ws=z(hq.hq_paged_attn_workspace_bytes(kv, B, H * G), dtype=torch.uint8))
+        row = s["qkv"].stride(0)
+
+        def step():
+            x = s["qkv"]
+            hq.hq_rope_kv_write(rope, kv, B, H * G, x, row, s["q"], H * G * D, x[:, H * G:], row, x[:, H * G + H:], row, s["pos"],
+                                table, P, s["slots"], glob, pages, s["buf"])
+            hq.hq_paged_attn(kv, B, H * G, s["q"], H * G * D, glob, pages, s["buf"], pt, most, s["lens"], 0.1, window, s["out"],
+                             H * G * D, s["lse"], s["ws"], s["ws"].numel())
+        return s, step
+
+    def feed(s, i):
+        at = torch.full((B,), i, device="cuda")
+        s["qkv"].copy_(steps[i])
+        s["pos"].copy_(at)
+        s["slots"].copy_(pt.long().gather(1, at[:, None] // page)[:, 0] * page + at % page)
+        s["lens"].copy_(at + 1)
+
+    (s, step), (e, eager) = program(), program()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i in range(len(steps)):
+        feed(s, i)
+        g.replay()
+        feed(e, i)
+        eager()
+        assert torch.equal(s["out"], e["out"]) and torch.equal(s["lse"], e["lse"]), i
+    assert hq.hq_device_error() == 0
+    # the last step against the formula, on what the cache holds by its recipe
+    first = len(steps) - window
+    pos = torch.arange(first, len(steps), device="cuda")
+    for b in range(B):
+        x = torch.stack([t[b] for t in steps[first:]])
+        k = turned(x[:, H * G:H * G + H], pos, table, D, 0)
+        k = k.to(torch.bfloat16).double() if dtype == "bf16" else held64(k, dtype, GLOB[0])
+        v = held64(x[:, H * G + H:], dtype, GLOB[1])
+        c = Paged.__new__(Paged)
+        c.dtype = dtype
+        for h in range(H):
+            r = slice(h * G, (h + 1) * G)
+            w = c._compare(s["q"][b, r].double(), k[:, h], v[:, h], 0.1, s["out"][b, r].double(), s["lse"][b, r].double())
+            assert torch.all(w <= 1), w
