@@ -458,3 +458,41 @@ def test_a_captured_step_follows_its_sequences(dtype, D):
             r = slice(h * G, (h + 1) * G)
             w = c._compare(s["q"][b, r].double(), k[:, h], v[:, h], 0.1, s["out"][b, r].double(), s["lse"][b, r].double())
             assert torch.all(w <= 1), w
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "nvfp4"])
+@pytest.mark.parametrize("D", [64, 192, 256])
+def test_every_bf16_number_is_held_as_the_activation_quantiser_has_it(dtype, D):
+    """All 65536 bit patterns, infinities and NaN among them, in rows of like sizes and of any: what is read back is what
+    hq_quant_act's codes and scales stand for."""
+    bits = torch.arange(65536, dtype=torch.int32, device="cuda")
+    rows = -(-65536 // D)
+    like = torch.cat([bits, bits[:rows * D - 65536]])
+    by_size = like[torch.argsort(like & 0x7FFF)]
+    mixed = like[torch.randperm(rows * D, generator=gen(151), device="cuda")]
+    x = torch.cat([by_size, mixed]).to(torch.int16).view(torch.bfloat16).reshape(2 * rows, 1, D).contiguous()
+    T, page = 2 * rows, 64
+    pages = -(-T // page)
+    kv = hq.KVDesc(dtype=DT[dtype], heads=1, head_dim=D, page_size=page)
+    buf = torch.zeros(pages * hq.hq_kv_page_bytes(kv), dtype=torch.uint8, device="cuda")
+    # E4M3 takes its scale from the row; both sides of NVFP4 under one second-level scale
+    glob = torch.tensor([2.5e-3, 2.5e-3], device="cuda") if dtype == "nvfp4" else None
+    slots = torch.arange(T, device="cuda")
+    hq.hq_kv_write(kv, T, x, D, x, D, slots, glob, pages, buf)
+    back = [torch.empty_like(x) for _ in range(2)]
+    hq.hq_kv_read(kv, T, slots, glob, pages, buf, back[0], D, back[1], D)
+    desc = hq.QuantDesc(w_dtype=hq.HQ_INT4, w_group=128, w_scale_dtype=hq.HQ_BF16, a_dtype=DT[dtype])
+    scales = torch.empty(T * D // 16, dtype=torch.uint8, device="cuda") if dtype == "nvfp4" else torch.empty(T, device="cuda")
+    codes = torch.empty(T, D if dtype == "e4m3" else D // 2, dtype=torch.uint8, device="cuda")
+    hq.hq_quant_act(desc, T, D, x, codes, scales, None, glob, None, 0)
+    if dtype == "e4m3":
+        want = codes.view(torch.float8_e4m3fn).float() * scales[:, None]
+    else:
+        grid = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6], device="cuda")
+        e = grid[torch.stack([codes & 15, codes >> 4], -1).long()].reshape(T, D // 16, 16)
+        want = (e * scales.view(torch.float8_e4m3fn).float().reshape(T, D // 16, 1) * glob[0]).reshape(T, D)
+    want = want.to(torch.bfloat16)
+    for got in back:
+        got = got[:, 0]
+        assert torch.equal(got.isnan(), want.isnan())
+        assert torch.equal(got.view(torch.int16)[~want.isnan()], want.view(torch.int16)[~want.isnan()])
