@@ -28,12 +28,15 @@
 //
 // Measured, of the floor of one read of the attended cache at 6.55 TB/s:
 // 64 x 8192 tokens x 8 heads x 128, E4M3 (1.09 GB) 170 us under a profiler,
-// 98%; 8 x ~107000 tokens, NVFP4 (1.01 GB) 205 to 215 us, 75% (364 instructions
-// a unit, over half of the issue slots: converting codes bounds it); ragged
-// batches of 0.3 GB 47 to 67 us of floor in 62 to 82 us, 51 to 78%: some 5 us
-// to the first unit, 5 to 8 to join, and SMs that end up to 15% apart.  One
-// sequence of 4097 tokens: 14.4 us, latency (each round trip through L2 in
-// the join is 1 to 2 us).
+// 98%; bf16 ragged to 8192 97% (three warps with 256 channels: 90%); 8 x
+// ~107000 tokens, NVFP4 (1.01 GB) 206 us, 75%.  There, issue slots are 0.61
+// used and the ALU pipe 61%, with four warps a scheduler of which 1.4 are
+// ready: too few for the chains of conversions and MMAs of a unit (324
+// instructions), and SMs idle 9% of the time at the ends.  Ragged batches of
+// 0.3 GB 47 to 67 us of floor in 62 to 81 us, 51 to 78%: some 5 us to the first
+// unit, 5 to 8 to join, and SMs that end up to 15% apart.  One sequence of 4097
+// tokens: 14.3 us, latency (each round trip through L2 in the join is 1 to
+// 2 us).
 //
 // Arithmetic.  Scores and sums are fp32.  bf16 caches multiply in bf16 with
 // each weight split into three bf16 numbers, together its 24 bits (two, 2^-17
